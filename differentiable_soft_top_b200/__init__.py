@@ -15,6 +15,9 @@ lambda = sum g f / sum f.
     p = lt.soft_topk(scores, k=1000.0, alpha=0.1)       # autograd-aware
     res = lt.forward(scores, 1000.0, 0.1, stats=True)   # p, b, sum f, status
     grad, dk = lt.backward(scores, g, res.b, 0.1)
+
+The operators of a layer of experts behind a router -- the hard choice of k
+experts per token, also by these memberships -- are in the module ``experts``.
 """
 from __future__ import annotations
 
@@ -156,26 +159,45 @@ def status_string(code: int) -> str:
     return _load().lapsum_status_string(int(code)).decode()
 
 
+def _experts_lib():
+    """The experts' library, if this process has loaded it (experts.py)."""
+    import sys
+    mod = sys.modules.get(__name__ + ".experts")
+    return mod._lib if mod is not None else None
+
+
 def launch_count() -> int:
-    """Kernels the native library has launched in this process."""
-    return int(_load().lapsum_launch_count())
+    """Kernels the native libraries have launched in this process."""
+    ex = _experts_lib()
+    return int(_load().lapsum_launch_count()) + (int(ex.lapsum_experts_launch_count()) if ex is not None else 0)
 
 
 def trace_enable(on: bool = True) -> None:
-    """Bracket every library kernel launch with CUDA events (see trace_collect)."""
+    """Bracket every library kernel launch with CUDA events (see trace_collect).
+    The experts' kernels are traced if experts.py has loaded its library."""
     _load().lapsum_trace_enable(1 if on else 0)
+    ex = _experts_lib()
+    if ex is not None:
+        ex.lapsum_experts_trace_enable(1 if on else 0)
+
+
+def _collect(fn) -> dict:
+    import json
+    need = fn(None, 0)
+    buf = ctypes.create_string_buffer(max(need, 2) + 64)
+    n = fn(buf, len(buf))
+    if n < 0:
+        raise RuntimeError("lapsum_trace_collect failed")
+    return {k: (int(v[0]), float(v[1])) for k, v in json.loads(buf.value.decode()).items()}
 
 
 def trace_collect() -> dict:
     """{kernel: (launches, total_ms)} of the launches traced since the last call."""
-    import json
-    lib = _load()
-    need = lib.lapsum_trace_collect(None, 0)
-    buf = ctypes.create_string_buffer(max(need, 2) + 64)
-    n = lib.lapsum_trace_collect(buf, len(buf))
-    if n < 0:
-        raise RuntimeError("lapsum_trace_collect failed")
-    return {k: (int(v[0]), float(v[1])) for k, v in json.loads(buf.value.decode()).items()}
+    got = _collect(_load().lapsum_trace_collect)
+    ex = _experts_lib()
+    if ex is not None:
+        got.update(_collect(ex.lapsum_experts_trace_collect))
+    return got
 
 
 def _params_ptr(params: Params | None):

@@ -1,0 +1,451 @@
+// exchange.cu -- between token order and expert order: the plan (a stable
+// counting sort of the slots by expert), the gather of token rows and the
+// weighted sum back, each with its gradient.
+//
+// All but the plan are bound by memory.  A warp takes a part of one row, 16
+// bytes per lane and access where the addresses allow it; short batches split
+// a row over several warps so that the GPU is full.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "experts.h"
+
+namespace lapsum {
+namespace {
+
+// ---- the plan ---------------------------------------------------------------------
+// A block sorts a range of `per` slots.  First kernel: a histogram per block.
+// Second: every block adds the histograms before its own and in all (at most
+// kMaxBlocks of them, one thread per expert), scans the experts, and places
+// its slots: each warp a contiguous part, 32 slots at a time in ascending
+// order, equal experts ranked by match_any.  Integer counts only.
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kMaxBlocks = 256;
+
+struct PlanShape {
+  int per, blocks;
+};
+PlanShape plan_shape(int64_t slots) {
+  // one block up to 4096 slots (one launch), then 2048 per block until there
+  // are kMaxBlocks
+  PlanShape p;
+  int64_t per = slots <= 4096 ? 4096 : std::max<int64_t>(2048, (slots + kMaxBlocks - 1) / kMaxBlocks);
+  per = (per + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
+  p.per = (int)per;
+  p.blocks = (int)((slots + per - 1) / per);
+  return p;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) k_plan_count(const int32_t* chosen, int64_t slots, int experts, int per,
+                                                             int32_t* hist) {
+  __shared__ int cnt[LAPSUM_EXPERTS_MAX];
+  for (int e = threadIdx.x; e < experts; e += kPlanThreads) cnt[e] = 0;
+  __syncthreads();
+  const int64_t s0 = (int64_t)blockIdx.x * per, s1 = min(slots, s0 + per);
+  for (int64_t s = s0 + threadIdx.x; s < s1; s += kPlanThreads) {
+    const int e = __ldg(chosen + s);
+    if ((unsigned)e < (unsigned)experts) atomicAdd(cnt + e, 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < experts; e += kPlanThreads) hist[(int64_t)blockIdx.x * experts + e] = cnt[e];
+}
+
+// hist == null: one block holds all slots
+__global__ void __launch_bounds__(kPlanThreads) k_plan_place(const int32_t* chosen, int64_t slots, int experts, int per,
+                                                             const int32_t* hist, int32_t* offsets, int32_t* rows,
+                                                             int32_t* slot_of) {
+  extern __shared__ int sh[];
+  int* total = sh;                       // [experts]
+  int* start = sh + experts;             // [experts] first row of this block's slots of an expert
+  int* mine = sh + 2 * experts;          // [warps][experts]
+  __shared__ int chunk[kPlanWarps + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t s0 = (int64_t)blockIdx.x * per, s1 = min(slots, s0 + per);
+  for (int i = threadIdx.x; i < kPlanWarps * experts; i += kPlanThreads) mine[i] = 0;
+  __syncthreads();
+  const int64_t part = per / kPlanWarps;  // a multiple of 32
+  const int64_t w0 = s0 + warp * part, w1 = min(s1, w0 + part);
+  int* cnt = mine + warp * experts;
+  for (int64_t s = w0 + lane; s < w1; s += 32) {
+    const int e = __ldg(chosen + s);
+    if ((unsigned)e < (unsigned)experts) atomicAdd(cnt + e, 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < experts; e += kPlanThreads) {
+    int run = 0;
+    for (int w = 0; w < kPlanWarps; ++w) {  // counts to starts within the block
+      const int c = mine[w * experts + e];
+      mine[w * experts + e] = run;
+      run += c;
+    }
+    int before = 0, all = run;
+    if (hist) {
+      all = 0;
+#pragma unroll 8
+      for (int b = 0; b < (int)gridDim.x; ++b) {
+        const int c = __ldg(hist + (int64_t)b * experts + e);
+        before += b < (int)blockIdx.x ? c : 0;
+        all += c;
+      }
+    }
+    total[e] = all;
+    start[e] = before;
+  }
+  __syncthreads();
+  // exclusive scan over the experts: kPlanThreads at a time
+  int base = 0;
+  for (int e0 = 0; e0 < experts; e0 += kPlanThreads) {
+    const int e = e0 + threadIdx.x;
+    const int own = e < experts ? total[e] : 0;
+    int v = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += u;
+    }
+    if (lane == 31) chunk[warp] = v;
+    __syncthreads();
+    int add = base;
+    for (int w = 0; w < warp; ++w) add += chunk[w];
+    int sum = 0;
+    for (int w = 0; w < kPlanWarps; ++w) sum += chunk[w];
+    if (e < experts) {
+      const int first = add + v - own;
+      start[e] += first;
+      if (blockIdx.x == 0) offsets[e] = first;
+    }
+    base += sum;
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) offsets[experts] = base;
+  // rows nobody owns
+  for (int64_t r = max(s0, (int64_t)base) + threadIdx.x; r < s1; r += kPlanThreads) slot_of[r] = -1;
+  for (int64_t g = w0; g < w1; g += 32) {
+    const int64_t s = g + lane;
+    int e = s < w1 ? __ldg(chosen + s) : -1;
+    if ((unsigned)e >= (unsigned)experts) e = -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    int row = -1;
+    if (e >= 0) row = start[e] + cnt[e] + __popc(same & ((1u << lane) - 1u));
+    __syncwarp();
+    if (e >= 0 && (same >> lane) == 1u) cnt[e] += __popc(same);  // the highest lane of its expert
+    __syncwarp();
+    if (s < w1) {
+      rows[s] = row;
+      if (row >= 0) slot_of[row] = (int)s;
+    }
+  }
+}
+
+// ---- rows ---------------------------------------------------------------------------
+constexpr int kRowThreads = 256;
+
+template <int kDtype>
+struct Elem;
+template <>
+struct Elem<LAPSUM_F32> {
+  using T = float;
+  static __device__ __forceinline__ float get(T v) { return v; }
+  static __device__ __forceinline__ T put(float v) { return v; }
+};
+template <>
+struct Elem<LAPSUM_BF16> {
+  using T = __nv_bfloat16;
+  static __device__ __forceinline__ float get(T v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ T put(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Elem<LAPSUM_F16> {
+  using T = __half;
+  static __device__ __forceinline__ float get(T v) { return __half2float(v); }
+  static __device__ __forceinline__ T put(float v) { return __float2half_rn(v); }
+};
+
+// kVec values moved together: 16 bytes, or one value where some address does
+// not lie on a 16-byte boundary
+template <int kDtype, int kVec>
+struct alignas(kVec * sizeof(typename Elem<kDtype>::T)) Pack {
+  typename Elem<kDtype>::T v[kVec];
+};
+template <int kDtype>
+constexpr int full_vec() {
+  return 16 / (int)sizeof(typename Elem<kDtype>::T);
+}
+
+template <int kDtype, int kVec>
+__device__ __forceinline__ Pack<kDtype, kVec> zero_pack() {
+  Pack<kDtype, kVec> p;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) p.v[i] = Elem<kDtype>::put(0.0f);
+  return p;
+}
+
+// The unit of work: warp `unit` takes part `unit % parts` of row `unit / parts`.
+struct Units {
+  int64_t rows;
+  int parts;
+  int per;  // packs per part
+  int packs;
+};
+
+template <int kDtype, int kVec>
+__global__ void __launch_bounds__(kRowThreads) k_dispatch(const typename Elem<kDtype>::T* __restrict__ x,
+                                                          int64_t x_stride, const int32_t* __restrict__ slot_of, int k,
+                                                          typename Elem<kDtype>::T* __restrict__ out, int64_t out_stride,
+                                                          int64_t slots, Units u) {
+  using P = Pack<kDtype, kVec>;
+  const int lane = threadIdx.x & 31;
+  const int64_t nwarp = (int64_t)gridDim.x * (kRowThreads / 32);
+  for (int64_t w = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); w < u.rows * u.parts; w += nwarp) {
+    const int64_t r = w / u.parts;
+    const int p0 = (int)(w - r * u.parts) * u.per, p1 = min(u.packs, p0 + u.per);
+    const int s = __ldg(slot_of + r);
+    const bool some = (uint64_t)(int64_t)s < (uint64_t)slots;
+    const P* src = reinterpret_cast<const P*>(x + (some ? s / k : 0) * x_stride);
+    P* dst = reinterpret_cast<P*>(out + r * out_stride);
+    for (int p = p0 + lane; p < p1; p += 128) {
+      P v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (p + 32 * i < p1) v[i] = some ? src[p + 32 * i] : zero_pack<kDtype, kVec>();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (p + 32 * i < p1) dst[p + 32 * i] = v[i];
+    }
+  }
+}
+
+template <int kDtype, int kVec>
+__global__ void __launch_bounds__(kRowThreads)
+    k_combine(const typename Elem<kDtype>::T* __restrict__ y, int64_t y_stride, const float* __restrict__ weights,
+              const int32_t* __restrict__ rows, int k, int64_t all_rows,
+              const typename Elem<kDtype>::T* __restrict__ residual, int64_t res_stride,
+              typename Elem<kDtype>::T* __restrict__ out, int64_t out_stride, Units u) {
+  using P = Pack<kDtype, kVec>;
+  const int lane = threadIdx.x & 31;
+  const int64_t nwarp = (int64_t)gridDim.x * (kRowThreads / 32);
+  for (int64_t w = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); w < u.rows * u.parts; w += nwarp) {
+    const int64_t t = w / u.parts;
+    const int p0 = (int)(w - t * u.parts) * u.per, p1 = min(u.packs, p0 + u.per);
+    int row = -1;
+    float wt = 0.0f;
+    if (lane < k) {
+      row = __ldg(rows + t * k + lane);
+      if ((uint64_t)(int64_t)row >= (uint64_t)all_rows) row = -1;
+      wt = weights ? __ldg(weights + t * k + lane) : (row >= 0 ? 1.0f : 0.0f);
+    }
+    for (int p = p0 + lane; p - lane < p1; p += 32) {
+      const bool on = p < p1;
+      float acc[kVec];
+      if (residual && on) {
+        const P v = reinterpret_cast<const P*>(residual + t * res_stride)[p];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) acc[i] = Elem<kDtype>::get(v.v[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) acc[i] = 0.0f;
+      }
+      for (int j0 = 0; j0 < k; j0 += 8) {
+        P v[8];
+        float c[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {  // up to 8 rows in flight
+          const int r = __shfl_sync(0xffffffffu, row, (j0 + j) & 31);
+          c[j] = __shfl_sync(0xffffffffu, wt, (j0 + j) & 31);
+          if (on && j0 + j < k && r >= 0)
+            v[j] = reinterpret_cast<const P*>(y + (int64_t)r * y_stride)[p];
+          else
+            v[j] = zero_pack<kDtype, kVec>();
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j0 + j < k) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) acc[i] = fmaf(c[j], Elem<kDtype>::get(v[j].v[i]), acc[i]);
+          }
+      }
+      if (on) {
+        P v;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v.v[i] = Elem<kDtype>::put(acc[i]);
+        reinterpret_cast<P*>(out + t * out_stride)[p] = v;
+      }
+    }
+  }
+}
+
+// One warp per slot: dY of its row and <g, y>.  Row numbers without a slot are
+// those a warp of the same number clears.
+template <int kDtype, int kVec>
+__global__ void __launch_bounds__(kRowThreads)
+    k_combine_bwd(const typename Elem<kDtype>::T* __restrict__ g, int64_t g_stride,
+                  const typename Elem<kDtype>::T* __restrict__ y, int64_t y_stride, const float* __restrict__ weights,
+                  const int32_t* __restrict__ rows, const int32_t* __restrict__ slot_of, int k, int64_t slots,
+                  typename Elem<kDtype>::T* __restrict__ gy, int64_t gy_stride, float* __restrict__ gw, int packs) {
+  using P = Pack<kDtype, kVec>;
+  const int lane = threadIdx.x & 31;
+  const int64_t nwarp = (int64_t)gridDim.x * (kRowThreads / 32);
+  for (int64_t s = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); s < slots; s += nwarp) {
+    int row = __ldg(rows + s);
+    if ((uint64_t)(int64_t)row >= (uint64_t)slots) row = -1;
+    const float wt = weights ? __ldg(weights + s) : 1.0f;
+    float dot = 0.0f;
+    if (row >= 0) {
+      const P* gp = reinterpret_cast<const P*>(g + s / k * g_stride);
+      const P* yp = reinterpret_cast<const P*>(y + (int64_t)row * y_stride);
+      P* op = reinterpret_cast<P*>(gy + (int64_t)row * gy_stride);
+      for (int p = lane; p < packs; p += 128) {
+        P a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (p + 32 * i < packs) {
+            a[i] = gp[p + 32 * i];
+            if (gw) b[i] = yp[p + 32 * i];
+          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (p + 32 * i < packs) {
+            P o;
+#pragma unroll
+            for (int q = 0; q < kVec; ++q) {
+              const float v = Elem<kDtype>::get(a[i].v[q]);
+              if (gw) dot = fmaf(v, Elem<kDtype>::get(b[i].v[q]), dot);
+              o.v[q] = Elem<kDtype>::put(wt * v);
+            }
+            if (gy) op[p + 32 * i] = o;
+          }
+      }
+    }
+    if (gw) {
+#pragma unroll
+      for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+      if (lane == 0) gw[s] = dot;
+    }
+    if (gy && __ldg(slot_of + s) < 0) {
+      P* op = reinterpret_cast<P*>(gy + s * gy_stride);
+      for (int p = lane; p < packs; p += 32) op[p] = zero_pack<kDtype, kVec>();
+    }
+  }
+}
+
+bool on16(const void* p, int64_t stride, int size) {
+  return !p || (!((uintptr_t)p & 15u) && !((stride * size) & 15));
+}
+
+Units make_units(int64_t rows, int64_t packs, int sms) {
+  Units u;
+  u.rows = rows;
+  u.packs = (int)packs;
+  // about 32 warps per SM, each with at least one access of all its lanes
+  const int64_t want = std::max<int64_t>(1, (int64_t)sms * 32 / std::max<int64_t>(1, rows));
+  const int64_t most = std::max<int64_t>(1, (packs + 31) / 32);
+  u.per = (int)((((packs + std::min(want, most) - 1) / std::min(want, most)) + 31) / 32 * 32);
+  u.parts = (int)((packs + u.per - 1) / u.per);
+  return u;
+}
+unsigned grid_of(int64_t warps, int sms) {
+  const int64_t blocks = (warps + kRowThreads / 32 - 1) / (kRowThreads / 32);
+  return (unsigned)std::max<int64_t>(1, std::min<int64_t>(blocks, (int64_t)sms * 64));
+}
+
+template <int kDtype, int kVec>
+void dispatch_as(const void* x, int64_t tokens, int k, int64_t dim, int64_t x_stride, const int32_t* slot_of, void* out,
+                 int64_t out_stride, int sms, cudaStream_t st) {
+  using T = typename Elem<kDtype>::T;
+  const Units u = make_units(tokens * k, dim / kVec, sms);
+  k_dispatch<kDtype, kVec><<<grid_of(u.rows * u.parts, sms), kRowThreads, 0, st>>>(
+      static_cast<const T*>(x), x_stride, slot_of, k, static_cast<T*>(out), out_stride, tokens * k, u);
+}
+template <int kDtype, int kVec>
+void combine_as(const void* y, int64_t tokens, int k, int64_t dim, int64_t y_stride, const float* weights,
+                const int32_t* rows, const void* residual, int64_t res_stride, void* out, int64_t out_stride, int sms,
+                cudaStream_t st) {
+  using T = typename Elem<kDtype>::T;
+  const Units u = make_units(tokens, dim / kVec, sms);
+  k_combine<kDtype, kVec><<<grid_of(u.rows * u.parts, sms), kRowThreads, 0, st>>>(
+      static_cast<const T*>(y), y_stride, weights, rows, k, tokens * k, static_cast<const T*>(residual), res_stride,
+      static_cast<T*>(out), out_stride, u);
+}
+template <int kDtype, int kVec>
+void combine_bwd_as(const void* grad, int64_t tokens, int k, int64_t dim, int64_t grad_stride, const void* y,
+                    int64_t y_stride, const float* weights, const int32_t* rows, const int32_t* slot_of, void* grad_y,
+                    int64_t grad_y_stride, float* grad_weights, int sms, cudaStream_t st) {
+  using T = typename Elem<kDtype>::T;
+  k_combine_bwd<kDtype, kVec><<<grid_of(tokens * k, sms), kRowThreads, 0, st>>>(
+      static_cast<const T*>(grad), grad_stride, static_cast<const T*>(y), y_stride, weights, rows, slot_of, k,
+      tokens * k, static_cast<T*>(grad_y), grad_y_stride, grad_weights, (int)(dim / kVec));
+}
+
+}  // namespace
+
+size_t plan_workspace(int64_t slots, int experts) {
+  const PlanShape p = plan_shape(slots);
+  return p.blocks > 1 ? (((size_t)p.blocks * experts * 4 + 255) & ~size_t(255)) : 0;
+}
+
+cudaError_t launch_plan(const int32_t* chosen, int64_t slots, int experts, int32_t* offsets, int32_t* rows,
+                        int32_t* slot_of, void* ws, cudaStream_t st) {
+  const PlanShape p = plan_shape(slots);
+  int32_t* hist = p.blocks > 1 ? static_cast<int32_t*>(ws) : nullptr;
+  if (hist) {
+    Launch guard("k_plan_count", st);
+    k_plan_count<<<p.blocks, kPlanThreads, 0, st>>>(chosen, slots, experts, p.per, hist);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  Launch guard("k_plan_place", st);
+  k_plan_place<<<p.blocks, kPlanThreads, (size_t)(2 + kPlanWarps) * experts * 4, st>>>(chosen, slots, experts, p.per,
+                                                                                     hist, offsets, rows, slot_of);
+  return cudaGetLastError();
+}
+
+cudaError_t exchange_init() {
+  return cudaFuncSetAttribute(k_plan_place, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (2 + kPlanWarps) * LAPSUM_EXPERTS_MAX * 4);
+}
+
+#define LAPSUM_BY_DTYPE(fn, vec, ...)                                             \
+  do {                                                                            \
+    if (dtype == LAPSUM_F32) {                                                    \
+      vec ? fn<LAPSUM_F32, full_vec<LAPSUM_F32>()>(__VA_ARGS__) : fn<LAPSUM_F32, 1>(__VA_ARGS__);    \
+    } else if (dtype == LAPSUM_BF16) {                                            \
+      vec ? fn<LAPSUM_BF16, full_vec<LAPSUM_BF16>()>(__VA_ARGS__) : fn<LAPSUM_BF16, 1>(__VA_ARGS__); \
+    } else {                                                                      \
+      vec ? fn<LAPSUM_F16, full_vec<LAPSUM_F16>()>(__VA_ARGS__) : fn<LAPSUM_F16, 1>(__VA_ARGS__);    \
+    }                                                                             \
+  } while (0)
+
+cudaError_t launch_dispatch(const void* x, int dtype, int64_t tokens, int k, int64_t dim, int64_t x_stride,
+                            const int32_t* slot_of, void* out, int64_t out_stride, int sms, cudaStream_t st) {
+  const int z = dtype == LAPSUM_F32 ? 4 : 2;
+  const bool vec = on16(x, x_stride, z) && on16(out, out_stride, z) && dim * z % 16 == 0;
+  Launch guard("k_dispatch", st);
+  LAPSUM_BY_DTYPE(dispatch_as, vec, x, tokens, k, dim, x_stride, slot_of, out, out_stride, sms, st);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_combine(const void* y, int dtype, int64_t tokens, int k, int64_t dim, int64_t y_stride,
+                           const float* weights, const int32_t* rows, const void* residual, int64_t res_stride,
+                           void* out, int64_t out_stride, int sms, cudaStream_t st) {
+  const int z = dtype == LAPSUM_F32 ? 4 : 2;
+  const bool vec = on16(y, y_stride, z) && on16(out, out_stride, z) && on16(residual, res_stride, z) && dim * z % 16 == 0;
+  Launch guard("k_combine", st);
+  LAPSUM_BY_DTYPE(combine_as, vec, y, tokens, k, dim, y_stride, weights, rows, residual, res_stride, out, out_stride,
+                  sms, st);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_combine_bwd(const void* grad, int dtype, int64_t tokens, int k, int64_t dim, int64_t grad_stride,
+                               const void* y, int64_t y_stride, const float* weights, const int32_t* rows,
+                               const int32_t* slot_of, void* grad_y, int64_t grad_y_stride, float* grad_weights,
+                               int sms, cudaStream_t st) {
+  const int z = dtype == LAPSUM_F32 ? 4 : 2;
+  const bool vec = on16(grad, grad_stride, z) && on16(y, y_stride, z) && on16(grad_y, grad_y_stride, z) && dim * z % 16 == 0;
+  Launch guard("k_combine_bwd", st);
+  LAPSUM_BY_DTYPE(combine_bwd_as, vec, grad, tokens, k, dim, grad_stride, y, y_stride, weights, rows, slot_of, grad_y,
+                  grad_y_stride, grad_weights, sms, st);
+  return cudaGetLastError();
+}
+
+}  // namespace lapsum
