@@ -52,10 +52,10 @@ cudaError_t launch_combine_bwd(const void* grad, int dtype, int64_t tokens, int 
                                const int32_t* slot_of, void* grad_y, int64_t grad_y_stride, float* grad_weights,
                                int sms, cudaStream_t st);
 
-// One launch of the experts' products (see linear.cu).
+// One launch of the experts' products (linear.cuh).
 struct Product {
   int64_t rows;
-  int experts, bf16, activation;
+  int experts, activation;
   int64_t in, out;             // of the weights
   const int32_t* offsets;      // or null: one expert owns all rows
   const void* x;               // forward, weight gradient: [rows, in]
@@ -73,11 +73,15 @@ struct Product {
   uint32_t* status;
 };
 // kernel attributes, once per device
-cudaError_t linear_init();
 cudaError_t exchange_init();
-cudaError_t launch_linear_fwd(const Product& p, int sms, cudaStream_t st);
-cudaError_t launch_linear_dx(const Product& p, int sms, cudaStream_t st);
-cudaError_t launch_linear_dweight(const Product& p, int sms, cudaStream_t st);
+cudaError_t linear_init_bf16();
+cudaError_t linear_init_f16();
+cudaError_t launch_linear_fwd_bf16(const Product& p, int sms, cudaStream_t st);
+cudaError_t launch_linear_fwd_f16(const Product& p, int sms, cudaStream_t st);
+cudaError_t launch_linear_dx_bf16(const Product& p, int sms, cudaStream_t st);
+cudaError_t launch_linear_dx_f16(const Product& p, int sms, cudaStream_t st);
+cudaError_t launch_linear_dweight_bf16(const Product& p, int sms, cudaStream_t st);
+cudaError_t launch_linear_dweight_f16(const Product& p, int sms, cudaStream_t st);
 
 size_t act_bwd_workspace(int64_t rows, int experts, int64_t out);
 cudaError_t launch_act_bwd(const void* grad_y, int bf16, int64_t rows, int64_t out, int64_t grad_y_stride,

@@ -46,7 +46,7 @@ int device_sms() {
     std::lock_guard<std::mutex> lk(g_mu);
     if (!d.ready.load(std::memory_order_relaxed)) {
       if (!cuda_ok(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev))) return 0;
-      if (!cuda_ok(linear_init()) || !cuda_ok(exchange_init())) return 0;
+      if (!cuda_ok(linear_init_bf16()) || !cuda_ok(linear_init_f16()) || !cuda_ok(exchange_init())) return 0;
       d.ready.store(true, std::memory_order_release);
     }
   }
@@ -70,9 +70,6 @@ constexpr int64_t kMaxIndex = INT32_MAX;
 bool matrix16(const void* p, int64_t cols, int64_t stride) {
   return p && aligned(p, 16) && stride >= cols && stride % 8 == 0 && stride < (int64_t(1) << 37);
 }
-// Any 16-bit matrix
-bool matrix2(const void* p, int64_t cols, int64_t stride) { return p && aligned(p, 2) && stride >= cols; }
-
 bool experts_shape(int experts, const int32_t* offsets) {
   return experts >= 1 && experts <= LAPSUM_EXPERTS_MAX && aligned(offsets, 4) && (offsets || experts == 1);
 }
@@ -249,8 +246,8 @@ int lapsum_experts_linear_fwd(const void* x, int dtype, int64_t rows, int64_t in
   if (gated && out % 16) return LAPSUM_EINVAL;
   if (!tiles_fit(rows, experts, in, out)) return LAPSUM_ETOOLARGE;
   const int64_t width = gated ? out / 2 : out;
-  if (!matrix16(x, in, x_stride) || !weight || !aligned(weight, 16) || !matrix2(y, width, y_stride)) return LAPSUM_EINVAL;
-  if ((residual && !matrix2(residual, width, residual_stride)) || (preact && !matrix2(preact, out, preact_stride)) ||
+  if (!matrix16(x, in, x_stride) || !weight || !aligned(weight, 16) || !matrix16(y, width, y_stride)) return LAPSUM_EINVAL;
+  if ((residual && !matrix16(residual, width, residual_stride)) || (preact && !matrix16(preact, out, preact_stride)) ||
       !aligned(bias, 2) || !aligned(status, 4))
     return LAPSUM_EINVAL;
   struct {
@@ -271,7 +268,6 @@ int lapsum_experts_linear_fwd(const void* x, int dtype, int64_t rows, int64_t in
   Product p{};
   p.rows = rows;
   p.experts = experts;
-  p.bf16 = dtype == LAPSUM_BF16;
   p.activation = activation;
   p.in = in;
   p.out = out;
@@ -287,7 +283,7 @@ int lapsum_experts_linear_fwd(const void* x, int dtype, int64_t rows, int64_t in
   p.preact = preact;
   p.preact_stride = preact_stride;
   p.status = status;
-  return done(launch_linear_fwd(p, sms, (cudaStream_t)stream));
+  return done((dtype == LAPSUM_BF16 ? launch_linear_fwd_bf16 : launch_linear_fwd_f16)(p, sms, (cudaStream_t)stream));
 }
 
 size_t lapsum_experts_linear_act_workspace_size(int64_t rows, int experts, int64_t out) {
@@ -334,7 +330,7 @@ int lapsum_experts_linear_dx(const void* grad_h, int dtype, int64_t rows, int64_
                              int64_t grad_x_stride, uint32_t* status, void* stream) {
   if (!linear_shape(dtype, rows, in, out) || !experts_shape(experts, offsets)) return LAPSUM_EINVAL;
   if (!tiles_fit(rows, experts, in, out)) return LAPSUM_ETOOLARGE;
-  if (!matrix16(grad_h, out, grad_h_stride) || !weight || !aligned(weight, 16) || !matrix2(grad_x, in, grad_x_stride) ||
+  if (!matrix16(grad_h, out, grad_h_stride) || !weight || !aligned(weight, 16) || !matrix16(grad_x, in, grad_x_stride) ||
       !aligned(status, 4))
     return LAPSUM_EINVAL;
   const size_t o = span(rows, in, grad_x_stride, 2);
@@ -347,7 +343,6 @@ int lapsum_experts_linear_dx(const void* grad_h, int dtype, int64_t rows, int64_
   Product p{};
   p.rows = rows;
   p.experts = experts;
-  p.bf16 = dtype == LAPSUM_BF16;
   p.in = in;
   p.out = out;
   p.offsets = offsets;
@@ -357,7 +352,7 @@ int lapsum_experts_linear_dx(const void* grad_h, int dtype, int64_t rows, int64_
   p.y = grad_x;
   p.y_stride = grad_x_stride;
   p.status = status;
-  return done(launch_linear_dx(p, sms, (cudaStream_t)stream));
+  return done((dtype == LAPSUM_BF16 ? launch_linear_dx_bf16 : launch_linear_dx_f16)(p, sms, (cudaStream_t)stream));
 }
 
 int lapsum_experts_linear_dweight(const void* grad_h, int dtype, int64_t rows, int64_t out, int64_t grad_h_stride,
@@ -378,7 +373,6 @@ int lapsum_experts_linear_dweight(const void* grad_h, int dtype, int64_t rows, i
   Product p{};
   p.rows = rows;
   p.experts = experts;
-  p.bf16 = dtype == LAPSUM_BF16;
   p.in = in;
   p.out = out;
   p.offsets = offsets;
@@ -388,7 +382,7 @@ int lapsum_experts_linear_dweight(const void* grad_h, int dtype, int64_t rows, i
   p.grad_h_stride = grad_h_stride;
   p.y = grad_weight;
   p.status = status;
-  return done(launch_linear_dweight(p, sms, (cudaStream_t)stream));
+  return done((dtype == LAPSUM_BF16 ? launch_linear_dweight_bf16 : launch_linear_dweight_f16)(p, sms, (cudaStream_t)stream));
 }
 
 }  // extern "C"

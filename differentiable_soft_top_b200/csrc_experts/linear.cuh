@@ -1,0 +1,920 @@
+// linear.cuh -- the experts' products and their gradients on the tensor cores.
+//
+// y_r = act(W_e x_r + b_e) + residual_r for the rows of expert e.  Rows are
+// few or many per expert and start anywhere, the features of a weight matrix
+// are many and regular; so the weights take the fixed side of the matrix
+// instruction (M = 128 of its rows) and the tokens the variable one (N = 16 ..
+// 256): D^T = W X^T.  A tile with 5 tokens then costs an N = 16 instruction,
+// not a 128-row one, and one kernel serves one token and long prompts.
+//
+//   forward          D[f, t] = sum_k W[f, k] X[t, k]       both K major
+//   input gradient   D[k, t] = sum_n W[n, k] dH[t, n]      W MN major
+//   weight gradient  D[n, k] = sum_t dH[t, n] X[t, k]      both MN major; the
+//                    contraction runs over an expert's rows and its ragged
+//                    end is zeroed in shared memory
+//
+// One block of six warps: warp 0 fills a ring of stages by tiled copies (64
+// deep, 128-byte swizzle), warp 1 issues the products, warps 2-5 read the
+// accumulators from tensor memory and write the result.  Two accumulators let
+// the epilogue of one tile run beside the products of the next; blocks walk
+// the tiles with a stride of the grid.  Three forms, by the rows of an expert:
+//   many   two blocks work as a pair on 256 features x 256 tokens: each copies
+//          its 128 features and half of the tokens, 32 KB per 64 of depth
+//          where a block alone would copy 48 KB, more than L2 delivers in the
+//          512 cycles of that product
+//   some   one block, 128 tokens
+//   few    one tile of 32 tokens per cluster of 1, 2, 4 or 8 blocks, which
+//          split the contraction and join their fp32 partials through
+//          distributed shared memory in the order of rank
+//
+// Gated weights (silu(gate) * up) are copied interleaved, 8 rows of one and 8
+// of the other, so that a thread holds the gate and the up value of a feature.
+// The epilogue reads accumulators as 8 x 8 fragments, which the transposing
+// stores turn into rows of the output in shared memory: global accesses are 16
+// bytes per lane.
+//
+// Every wait is bounded: a block that gives up sets a status bit, writes NaN
+// for what it leaves undone, lets its copies land and frees its tensor memory.
+#pragma once
+
+#include <type_traits>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "experts.h"
+#include "umma.cuh"
+
+namespace lapsum {
+namespace {
+
+enum Mode { kForward, kGradX, kGradW };
+
+constexpr int kThreads = 192;
+constexpr int kDepth = 64;              // contraction per stage: one 128-byte line
+constexpr int kLanes = 128;             // accumulator lanes of a block
+constexpr int kTokBox = 32;             // tokens per copied box
+constexpr uint32_t kPolls = 1u << 22;   // polls of a bounded wait, about a second
+constexpr int kPitch = 80;              // bytes between staged rows of 64: conflict-free
+
+struct Args {
+  int64_t rows;
+  int experts, activation;
+  int feat;          // features of the output (half of the weights' rows when gated)
+  int depth;         // contraction length (kGradW: set per tile)
+  int cols;          // kGradW: columns of the weight gradient
+  const int32_t* offsets;
+  const void* bias;
+  const void* residual;
+  int64_t residual_stride;
+  void* y;
+  int64_t y_stride;
+  void* preact;
+  int64_t preact_stride;
+  uint32_t* status;
+};
+
+template <int kMode, int kTok, bool kGated>
+struct Shape {
+  static constexpr bool kPair = kTok == 256;
+  static constexpr bool kSplit = kTok == 32;       // few rows: clusters, two blocks per SM
+  static constexpr int kFeat = kLanes / (kGated ? 2 : 1);           // features of a block's tile
+  static constexpr int kTileFeat = kFeat * (kPair ? 2 : 1);         // of a tile
+  static constexpr int kABytes = kLanes * 128;
+  static constexpr int kBBytes = (kPair ? kTok / 2 : kTok) * 128;
+  static constexpr int kStage = kABytes + kBBytes;
+  static constexpr int kBudget = kSplit ? 100 * 1024 : 196 * 1024;
+  static constexpr int kStages = kBudget / kStage;
+  static constexpr int kTmemCols = kSplit ? 32 : 2 * kTok;
+  static constexpr int kStaging = kSplit ? 0 : 4 * 32 * kPitch;  // the split form stages in the ring
+  static constexpr int kTable = kMode == kGradW ? 0 : (LAPSUM_EXPERTS_MAX + 2) * 4;
+  static constexpr int kSmem = kStages * kStage + kStaging + kTable + 1024 /* alignment */ + 512 /* barriers */;
+};
+
+// ---- 16-bit values ------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <typename T>
+__device__ __forceinline__ float load1(const void* p, int64_t i) {
+  return unpack2<T>((uint32_t)__ldg(static_cast<const uint16_t*>(p) + i)).x;
+}
+
+// ---- activations ----------------------------------------------------------------------
+__device__ __forceinline__ float sigmoid_of(float h) { return __fdividef(1.0f, 1.0f + __expf(-h)); }
+
+// The normal CDF by the rational approximation 7.1.26 of Abramowitz & Stegun
+// (|error| of erf <= 1.5e-7): 0.5 erfc(|h| / sqrt 2) = t P(t) exp(-h^2/2) / 2
+// with t = 1 / (1 + 0.3275911 |h| / sqrt 2).  The lower tail is not a difference.
+__device__ __forceinline__ float normal_cdf(float h) {
+  const float t = __fdividef(1.0f, fmaf(0.23164189f, fabsf(h), 1.0f));
+  float p = fmaf(t, 1.061405429f, -1.453152027f);
+  p = fmaf(t, p, 1.421413741f);
+  p = fmaf(t, p, -0.284496736f);
+  p = fmaf(t, p, 0.254829592f);
+  const float q = 0.5f * p * t * __expf(-0.5f * h * h);
+  return h < 0.0f ? q : 1.0f - q;
+}
+
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
+  if (act == LAPSUM_ACT_RELU) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) v[c] = v[c] < 0.0f ? 0.0f : v[c];  // keeps NaN
+  } else if (act == LAPSUM_ACT_SILU) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) v[c] *= sigmoid_of(v[c]);
+  } else if (act == LAPSUM_ACT_GELU) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) v[c] *= normal_cdf(v[c]);
+  }
+}
+
+// ---- tiles ------------------------------------------------------------------------------
+struct Tile {
+  int expert;
+  int row0, n;   // tokens [row0, row0 + n) (kGradW: the expert's rows)
+  int f0;        // first feature of this block
+  int c0;        // kGradW: first column
+  int chunks;    // stages of this tile's contraction (0: nothing to multiply)
+};
+
+// Row range of expert e, clamped into the array whatever the offsets hold;
+// "expert" a.experts is the rows behind the last one's.
+__device__ __forceinline__ void row_range(const Args& a, int e, int& lo, int& n) {
+  const int rows = (int)a.rows;
+  int hi = rows;
+  if (a.offsets) {
+    lo = min(max(__ldg(a.offsets + e), 0), rows);
+    if (e < a.experts) hi = min(max(__ldg(a.offsets + e + 1), 0), rows);
+  } else {
+    lo = e ? rows : 0;
+  }
+  n = max(hi - lo, 0);
+}
+
+// Token tiles before each expert, in shared memory: table[e] for e = 0 ..
+// experts + 1 (one warp).
+template <int kTok>
+__device__ __forceinline__ void build_table(const Args& a, int* table, int lane) {
+  int base = 0;
+  for (int e0 = 0; e0 <= a.experts; e0 += 32) {
+    const int e = e0 + lane;
+    int lo = 0, n = 0;
+    if (e <= a.experts) row_range(a, e, lo, n);
+    int v = (n + kTok - 1) / kTok;
+    const int own = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += u;
+    }
+    if (e <= a.experts) table[e] = base + v - own;
+    base += __shfl_sync(0xffffffffu, v, 31);
+  }
+  if (lane == 0) table[a.experts + 1] = base;
+}
+
+template <int kMode, int kTok, bool kGated>
+__device__ __forceinline__ Tile tile_of(const Args& a, const int* table, int tile, int half) {
+  using S = Shape<kMode, kTok, kGated>;
+  Tile t;
+  const int ftiles = (a.feat + S::kTileFeat - 1) / S::kTileFeat;
+  t.c0 = 0;
+  if (kMode == kGradW) {
+    const int ctiles = (a.cols + kTok - 1) / kTok;
+    t.expert = tile / (ftiles * ctiles);
+    const int in = tile - t.expert * (ftiles * ctiles);
+    t.f0 = (in / ctiles) * S::kTileFeat + half * S::kFeat;
+    t.c0 = (in % ctiles) * kTok;
+    row_range(a, t.expert, t.row0, t.n);
+    t.chunks = (t.n + kDepth - 1) / kDepth;
+    return t;
+  }
+  const int tt = tile / ftiles;
+  t.f0 = (tile - tt * ftiles) * S::kTileFeat + half * S::kFeat;
+  int lo = 0, hi = a.experts;  // the last expert whose first tile is <= tt
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (table[mid] <= tt) lo = mid; else hi = mid - 1;
+  }
+  t.expert = lo;
+  int row0, n;
+  row_range(a, lo, row0, n);
+  const int skip = (tt - table[lo]) * kTok;
+  t.row0 = row0 + skip;
+  t.n = min(n - skip, kTok);
+  t.chunks = lo < a.experts ? (a.depth + kDepth - 1) / kDepth : 0;
+  return t;
+}
+
+// ---- bounded waits: a block that has given up somewhere gives up everywhere --------------
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile uint32_t* gave_up) {
+  for (uint32_t i = 0; i < kPolls; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 63u && *gave_up) return false;
+  }
+  *gave_up = 1u;
+  return false;
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile uint32_t* gave_up) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return wait_slow(bar, parity, gave_up);
+}
+
+// ---- epilogue: a warp's 32 accumulator lanes x 32 columns --------------------------------
+// v[h]: the fragments of lanes 16 h .. 16 h + 15 (tmem_load_16x32).  Without
+// gates lane = feature; with gates lanes 16 h + 0..7 are the gates and + 8..15 the
+// ups of features 8 h .. 8 h + 7.  p[j]: packed pairs of tokens 8 j + c, + 1 of the
+// feature groups (of 8) in order: 4 (2 with gates) per token group j.
+template <bool kGated>
+struct Frag {
+  static constexpr int kGroups = kGated ? 2 : 4;
+  uint32_t p[4][kGroups];
+};
+
+// bytes from the staging area: token `tok`, feature group `g`
+__device__ __forceinline__ uint32_t staged(uint32_t base, int tok, int g) { return base + tok * kPitch + g * 16; }
+
+template <bool kGated>
+__device__ __forceinline__ uint32_t lane_row(uint32_t base, int jj, int lane) {
+  const int m = lane >> 3;
+  return kGated ? staged(base, 8 * (jj + (m >> 1)) + (lane & 7), m & 1) : staged(base, 8 * jj + (lane & 7), m);
+}
+
+// fragments -> rows of dst (16 bytes per lane).  own: which (token group j,
+// lane half h) pieces are this block's to write, bit 2 j + h.
+template <bool kGated>
+__device__ __forceinline__ void put(const Frag<kGated>& f, uint32_t base, void* dst, int64_t row, int64_t stride, int feat0,
+                                    int feat, int n, uint32_t own, int lane) {
+  constexpr int G = Frag<kGated>::kGroups;
+  if (kGated) {
+#pragma unroll
+    for (int j = 0; j < 4; j += 2)
+      stage_4<true>(lane_row<kGated>(base, j, lane), f.p[j][0], f.p[j][1], f.p[j + 1][0], f.p[j + 1][1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      stage_4<true>(lane_row<kGated>(base, j, lane), f.p[j][0], f.p[j][1], f.p[j][2 % G], f.p[j][3 % G]);
+  }
+  __syncwarp();
+  uint16_t* out = static_cast<uint16_t*>(dst);
+#pragma unroll
+  for (int it = 0; it < G; ++it) {
+    const int tok = it * (32 / G) + lane / G, g = lane % G;
+    const int h = kGated ? g : g >> 1;
+    const uint4 v = lds16(staged(base, tok, g));
+    if (tok < n && feat0 + 8 * g < feat && (own >> (2 * (tok >> 3) + h) & 1u))
+      *reinterpret_cast<uint4*>(out + (row + tok) * stride + feat0 + 8 * g) = v;
+  }
+  __syncwarp();
+}
+
+// rows of src, one chunk: loads only
+template <bool kGated>
+__device__ __forceinline__ void get_rows(uint4 (&q)[Frag<kGated>::kGroups], const void* src, int64_t row, int64_t stride,
+                                         int feat0, int feat, int n, int lane) {
+  constexpr int G = Frag<kGated>::kGroups;
+  const uint16_t* in = static_cast<const uint16_t*>(src);
+#pragma unroll
+  for (int it = 0; it < G; ++it) {
+    const int tok = it * (32 / G) + lane / G, g = lane % G;
+    q[it] = make_uint4(0u, 0u, 0u, 0u);
+    if (tok < n && feat0 + 8 * g < feat)
+      q[it] = __ldg(reinterpret_cast<const uint4*>(in + (row + tok) * stride + feat0 + 8 * g));
+  }
+}
+
+// 32 tokens of a warp's features: bias, activation, residual, store
+template <typename T, bool kGated>
+__device__ __forceinline__ void finish(const Args& a, const Tile& t, int c0, int feat0, const float (&bias)[4],
+                                       float (&v)[2][16], const uint4 (&res)[Frag<kGated>::kGroups], uint32_t base,
+                                       uint32_t own, int lane) {
+  constexpr int G = Frag<kGated>::kGroups;
+  const int n = min(32, t.n - c0);
+  const int64_t row = t.row0 + c0;
+  const bool multiplied = t.expert < a.experts;
+  Frag<kGated> f;
+  float o[4][G][2];
+  if (multiplied) {
+    if (a.bias) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[h][i] += bias[2 * h + (i >> 1 & 1)];
+    }
+    if (a.preact) {
+      if (kGated) {
+#pragma unroll
+        for (int up = 0; up < 2; ++up) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) f.p[j][h] = pack2<T>(v[h][4 * j + 2 * up], v[h][4 * j + 2 * up + 1]);
+          put<kGated>(f, base, static_cast<uint16_t*>(a.preact) + up * a.feat, row, a.preact_stride, feat0, a.feat, n, own,
+                      lane);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+            f.p[j][g] = pack2<T>(v[g >> 1][4 * j + 2 * (g & 1)], v[g >> 1][4 * j + 2 * (g & 1) + 1]);
+        put<kGated>(f, base, a.preact, row, a.preact_stride, feat0, a.feat, n, own, lane);
+      }
+    }
+    if (kGated) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float g = v[h][4 * j + i];
+            o[j][h][i] = g * sigmoid_of(g) * v[h][4 * j + 2 + i];
+          }
+    } else {
+      activate(v[0], a.activation);
+      activate(v[1], a.activation);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) o[j][g][i] = v[g >> 1][4 * j + 2 * (g & 1) + i];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int g = 0; g < G; ++g) o[j][g][0] = o[j][g][1] = 0.0f;
+  }
+  if (a.residual) {  // rows -> fragments
+#pragma unroll
+    for (int it = 0; it < G; ++it) sts16(staged(base, it * (32 / G) + lane / G, lane % G), res[it]);
+    __syncwarp();
+    uint32_t r[4];
+#pragma unroll
+    for (int j = 0; j < 4; j += kGated ? 2 : 1) {
+      fetch_4_trans(lane_row<kGated>(base, j, lane), r[0], r[1], r[2], r[3]);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const float2 w = unpack2<T>(r[m]);
+        float* to = kGated ? o[j + (m >> 1)][m & 1] : o[j][m % G];
+        to[0] += w.x;
+        to[1] += w.y;
+      }
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int g = 0; g < G; ++g) f.p[j][g] = pack2<T>(o[j][g][0], o[j][g][1]);
+  put<kGated>(f, base, a.y, row, a.y_stride, feat0, a.feat, n, own, lane);
+}
+
+// 32 columns of a warp's 32 rows of a weight gradient
+template <typename T>
+__device__ __forceinline__ void finish_grad_w(const Args& a, const Tile& t, int c0, int feat0, const float (&v)[2][16],
+                                              uint32_t base, int lane) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int r = 0; r < 2; ++r)  // 8 rows, four groups of 8 columns
+      stage_4<false>(staged(base, 16 * h + 8 * r + (lane & 7), lane >> 3), pack2<T>(v[h][2 * r], v[h][2 * r + 1]),
+                     pack2<T>(v[h][4 + 2 * r], v[h][5 + 2 * r]), pack2<T>(v[h][8 + 2 * r], v[h][9 + 2 * r]),
+                     pack2<T>(v[h][12 + 2 * r], v[h][13 + 2 * r]));
+  __syncwarp();
+  uint16_t* out = static_cast<uint16_t*>(a.y);
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int r = it * 8 + lane / 4, col = t.c0 + c0 + 8 * (lane & 3);
+    const uint4 w = lds16(staged(base, r, lane & 3));
+    if (feat0 + r < a.feat && col < a.cols)
+      *reinterpret_cast<uint4*>(out + ((int64_t)t.expert * a.feat + feat0 + r) * a.cols + col) = w;
+  }
+  __syncwarp();
+}
+
+template <typename T, bool kGated>
+__device__ __forceinline__ void load_bias(const Args& a, const Tile& t, int feat0, float (&b)[4], int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = 0.0f;
+  if (!a.bias || t.expert >= a.experts) return;
+  const int64_t at = (int64_t)t.expert * a.feat * (kGated ? 2 : 1);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int f = feat0 + (kGated ? 8 * (i >> 1) : 8 * i) + lane / 4;
+    if (f < a.feat) b[i] = load1<T>(a.bias, at + f + (kGated && (i & 1) ? a.feat : 0));
+  }
+}
+
+__device__ __forceinline__ void fill(float (&v)[2][16], float x) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = x;
+}
+
+// map_f: the weights (kGradW: dH); map_t: the tokens' rows
+template <typename T, int kMode, int kTok, bool kGated>
+__global__ void __launch_bounds__(kThreads, Shape<kMode, kTok, kGated>::kSplit ? 2 : 1)
+    k_product(const __grid_constant__ CUtensorMap map_f, const __grid_constant__ CUtensorMap map_t, const Args a,
+              int tiles_grad_w) {
+  using S = Shape<kMode, kTok, kGated>;
+  constexpr int kStages = S::kStages;
+  constexpr bool kPair = S::kPair;
+  extern __shared__ unsigned char smem_raw[];
+  // operands in the 128-byte swizzle start on 1024-byte boundaries
+  unsigned char* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned char* staging = ring + kStages * S::kStage;
+  unsigned char* tail = staging + S::kStaging;
+  uint64_t* full = reinterpret_cast<uint64_t*>(tail);
+  uint64_t* empty = full + kStages;
+  uint64_t* peer_full = empty + kStages;  // kPair, first block: the second's stage has landed
+  uint64_t* acc_full = peer_full + kStages;  // [2]
+  uint64_t* acc_empty = acc_full + 2;        // [2]
+  uint64_t* drained = acc_empty + 2;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile uint32_t* gave_up = tmem_at + 1;
+  int* table = reinterpret_cast<int*>(tail + 512);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int half = kPair ? (int)cluster_rank() : 0;
+  if (threadIdx.x == 0) {
+    prefetch_map(&map_f);
+    prefetch_map(&map_t);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+      mbar_init(peer_full + s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full + b, 1);
+      mbar_init(acc_empty + b, kPair ? 8 : 4);
+    }
+    mbar_init(drained, 1);
+    *gave_up = 0u;
+  }
+  if (warp == 1) tmem_alloc<kPair>(tmem_at, S::kTmemCols);
+  if (kMode != kGradW && warp == 2) build_table<kTok>(a, table, lane);
+  tc_fence_before();
+  __syncthreads();
+  if (kPair) cluster_sync();  // the other block's barriers are set up
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+
+  const int ftiles = (a.feat + S::kTileFeat - 1) / S::kTileFeat;
+  const int tiles = kMode == kGradW ? tiles_grad_w : table[a.experts + 1] * ftiles;
+  const int ranks = S::kSplit ? (int)cluster_size() : kPair ? 2 : 1;
+  const int rank = S::kSplit ? (int)cluster_rank() : 0;
+  // few rows: the grid holds a cluster for every tile there can be
+  const int first = (int)blockIdx.x / ranks, step = S::kSplit ? max(tiles, 1) : (int)gridDim.x / ranks;
+
+  // kSplit: this block's share of a tile's contraction
+  auto share = [&](const Tile& t, int& c0, int& c1) {
+    if (!S::kSplit) {
+      c0 = 0;
+      c1 = t.chunks;
+      return;
+    }
+    const int per = (t.chunks + ranks - 1) / ranks;
+    c0 = min(rank * per, t.chunks);
+    c1 = min(c0 + per, t.chunks);
+  };
+  // variable side of the instruction, and the part of it this block copies
+  auto width = [&](const Tile& t, int& n, int& n0, int& own) {
+    const int all = kMode == kGradW ? min(kTok, a.cols - t.c0) : t.n;
+    n = kPair ? (all + 31) & ~31 : (all + 15) & ~15;
+    n0 = half * (n / 2);
+    own = kPair ? min(n / 2, max(all - n0, 0)) : all;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int tile = first; ok && tile < tiles; tile += step) {
+        const Tile t = tile_of<kMode, kTok, kGated>(a, table, tile, half);
+        int c0, c1, n, n0, own;
+        share(t, c0, c1);
+        width(t, n, n0, own);
+        constexpr int kBox = kMode == kGradW ? 64 : kTokBox, kBoxBytes = kMode == kGradW ? 8192 : kTokBox * 128;
+        const int boxes = (own + kBox - 1) / kBox;
+        const uint32_t bytes = S::kABytes + boxes * kBoxBytes;
+        for (int c = c0; c < c1; ++c, ++it) {
+          const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
+          if (!wait_for(empty + s, ph ^ 1u, gave_up)) {
+            ok = false;
+            break;
+          }
+          unsigned char* sa = ring + s * S::kStage;
+          unsigned char* sb = sa + S::kABytes;
+          const int d = c * kDepth;
+          mbar_arrive_expect_tx(full + s, bytes);
+          if (kMode == kForward) {
+            if (kGated)
+              tma_load_5d(sa, &map_f, d, 0, 0, t.f0 / 8, t.expert, full + s);
+            else
+              tma_load_3d(sa, &map_f, d, t.f0, t.expert, full + s);
+          } else if (kMode == kGradX) {
+            tma_load_3d(sa, &map_f, t.f0, d, t.expert, full + s);
+            tma_load_3d(sa + 8192, &map_f, t.f0 + 64, d, t.expert, full + s);
+          } else {
+            tma_load_2d(sa, &map_f, t.f0, t.row0 + d, full + s);
+            tma_load_2d(sa + 8192, &map_f, t.f0 + 64, t.row0 + d, full + s);
+          }
+          for (int b = 0; b < boxes; ++b) {
+            if (kMode == kGradW)
+              tma_load_2d(sb + b * kBoxBytes, &map_t, t.c0 + n0 + kBox * b, t.row0 + d, full + s);
+            else
+              tma_load_2d(sb + b * kBoxBytes, &map_t, d, t.row0 + n0 + kBox * b, full + s);
+          }
+        }
+      }
+      // before the block ends, its copies in flight land (bounded); after a
+      // normal end warp 1 has waited for every one of them
+      if (!ok) {
+        for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0u; j < it; ++j)
+          mbar_wait_bounded(full + j % kStages, (j / kStages) & 1u, kPolls);
+      }
+    }
+  } else if (warp == 1) {
+    uint32_t it = 0, done = 0;
+    bool ok = true;
+    for (int tile = first; ok && tile < tiles; tile += step) {
+      const Tile t = tile_of<kMode, kTok, kGated>(a, table, tile, half);
+      int c0, c1, n, n0, own;
+      share(t, c0, c1);
+      width(t, n, n0, own);
+      if (c0 == c1) continue;
+      const uint32_t buf = S::kSplit ? 0u : done & 1u;
+      if (half == 0) {
+        ok = __all_sync(0xffffffffu,
+                        wait_for(acc_empty + buf, ((S::kSplit ? done : done >> 1) & 1u) ^ 1u, gave_up));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const uint32_t acc = tmem + buf * kTok;
+      const uint32_t idesc =
+          instr_desc(std::is_same<T, __nv_bfloat16>::value, kMode != kForward, kMode == kGradW, kLanes * (kPair ? 2 : 1), n);
+      for (int c = c0; c < c1; ++c, ++it) {
+        const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
+        ok = __all_sync(0xffffffffu, wait_for(full + s, ph, gave_up));
+        if (!ok) break;
+        unsigned char* sa = ring + s * S::kStage;
+        unsigned char* sb = sa + S::kABytes;
+        if (kMode == kGradW) {
+          // lines of rows behind the expert's last one: zero in both operands
+          // (whatever they held, NaN included, must not reach the sums)
+          const int left = t.n - c * kDepth;
+          if (left < kDepth) {
+            const int lines = kDepth - left, blocks = 2 + (own + 63) / 64;
+            for (int i = lane; i < blocks * lines * 8; i += 32) {
+              const int line = i >> 3, blk = line / lines;
+              *reinterpret_cast<uint4*>(sa + blk * 8192 + (left + line - blk * lines) * 128 + (i & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        if (half != 0) {  // the first block issues for both
+          if (lane == 0) {
+            if (kMode == kGradW && t.n - c * kDepth < kDepth)
+              arrive_at<true>(peer_full + s, 0);
+            else
+              arrive_at<false>(peer_full + s, 0);
+          }
+          continue;
+        }
+        if (kPair) {
+          ok = __all_sync(0xffffffffu, wait_for(peer_full + s, ph, gave_up));
+          if (!ok) break;
+          if (kMode == kGradW && t.n - c * kDepth < kDepth) acquire_cluster();
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t da = operand_desc(smem_u32(sa), kMode == kForward ? 16u : 8192u);
+          const uint64_t db = operand_desc(smem_u32(sb), kMode == kGradW ? 8192u : 16u);
+          constexpr uint32_t kStepA = (kMode == kForward ? 32 : 2048) >> 4, kStepB = (kMode == kGradW ? 2048 : 32) >> 4;
+#pragma unroll
+          for (uint32_t k = 0; k < kDepth / 16; ++k)
+            mma_f16<kPair>(acc, da + k * kStepA, db + k * kStepB, idesc, c != c0 || k != 0);
+          mma_commit<kPair>(empty + s);
+          if (c + 1 == c1) mma_commit<kPair>(acc_full + buf);
+        }
+        __syncwarp();
+      }
+      ++done;
+    }
+    if (!ok && half == 0) {  // the products in flight end before their tensor memory is freed
+      if (lane == 0) mma_commit<kPair>(drained);
+      __syncwarp();
+      mbar_wait_bounded(drained, 0u, kPolls);
+    }
+  } else if (!S::kSplit) {
+    const int quarter = warp & 3;  // the lanes of tensor memory this warp may read
+    const uint32_t base = smem_u32(staging) + quarter * 32 * kPitch;
+    uint32_t done = 0;
+    bool ok = true;
+    for (int tile = first; tile < tiles; tile += step) {
+      const Tile t = tile_of<kMode, kTok, kGated>(a, table, tile, half);
+      const int feat0 = t.f0 + quarter * (S::kFeat / 4);
+      const uint32_t buf = done & 1u;
+      const bool sums = t.chunks > 0;
+      const int n = kMode == kGradW ? min(kTok, a.cols - t.c0) : t.n;
+      float bias[4];
+      uint4 res[Frag<kGated>::kGroups];
+      if (kMode == kForward) {
+        load_bias<T, kGated>(a, t, feat0, bias, lane);
+        if (a.residual) get_rows<kGated>(res, a.residual, t.row0, a.residual_stride, feat0, a.feat, n, lane);
+      }
+      if (sums) {
+        ok = ok && __all_sync(0xffffffffu, wait_for(acc_full + buf, (done >> 1) & 1u, gave_up));
+        tc_fence_after();
+      }
+      const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTok;
+      for (int c0 = 0; c0 < n; c0 += 32) {
+        float v[2][16];
+        if (sums && ok) {
+          tmem_load_16x32(acc + c0, v[0]);
+          tmem_load_16x32(acc + (16u << 16) + c0, v[1]);
+          tmem_load_wait();
+          if (c0 + 32 >= n) {  // all columns are in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (kPair) arrive_at<false>(acc_empty + buf, 0);
+              else mbar_arrive(acc_empty + buf);
+            }
+          }
+        } else {
+          fill(v, ok ? 0.0f : __int_as_float(0x7fc00000));
+        }
+        if constexpr (kMode == kGradW) {
+          finish_grad_w<T>(a, t, c0, feat0, v, base, lane);
+        } else {
+          uint4 cur[Frag<kGated>::kGroups];
+#pragma unroll
+          for (int i = 0; i < Frag<kGated>::kGroups; ++i) cur[i] = res[i];
+          if (kMode == kForward && a.residual && c0 + 32 < n)  // the next chunk's, while this one is worked on
+            get_rows<kGated>(res, a.residual, t.row0 + c0 + 32, a.residual_stride, feat0, a.feat, n - c0 - 32, lane);
+          finish<T, kGated>(a, t, c0, feat0, bias, v, cur, base, 0xffu, lane);
+        }
+      }
+      if (sums) ++done;
+    }
+  }
+
+  if constexpr (S::kSplit) {
+    // one tile per cluster: the ranks' partials meet in shared memory
+    __syncwarp();
+    const bool busy = first < tiles;  // the same for all ranks of the cluster
+    if (busy) {
+      const Tile t = tile_of<kMode, kTok, kGated>(a, table, first, 0);
+      int s0, s1;
+      share(t, s0, s1);
+      const int quarter = warp & 3;
+      const int feat0 = t.f0 + quarter * (S::kFeat / 4);
+      float v[2][16], bias[4];
+      uint4 res[Frag<kGated>::kGroups];
+      // every product has read its operands (acc_full), so the ring is free
+      float* red = reinterpret_cast<float*>(ring) + quarter * 1024 + lane;  // [warp][value][lane]
+      const uint32_t base = smem_u32(ring) + 16384 + quarter * 32 * kPitch;
+      bool ok = true;
+      if (warp >= 2) {
+        load_bias<T, kGated>(a, t, feat0, bias, lane);
+        if (a.residual) get_rows<kGated>(res, a.residual, t.row0, a.residual_stride, feat0, a.feat, t.n, lane);
+        if (s0 < s1) {
+          ok = __all_sync(0xffffffffu, wait_for(acc_full, 0u, gave_up));
+          tc_fence_after();
+        }
+        if (s0 < s1 && ok) {
+          const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16);
+          tmem_load_16x32(acc, v[0]);
+          tmem_load_16x32(acc + (16u << 16), v[1]);
+          tmem_load_wait();
+        } else {
+          fill(v, ok ? 0.0f : __int_as_float(0x7fc00000));
+        }
+        if (ranks > 1) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (8 * ((i & 15) >> 2) < t.n) red[32 * i] = v[i >> 4][i & 15];
+        }
+      }
+      uint32_t own = 0xffu;
+      if (ranks > 1) {
+        __syncwarp();
+        cluster_sync();
+        // this rank finishes every ranks-th piece of 8 tokens x 16 lanes
+        own = ranks == 8 ? 1u << rank : ranks == 4 ? 0x11u << rank : 0x55u << rank;
+        if (warp >= 2) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int j = (i & 15) >> 2, h = i >> 4;
+            float sum = 0.0f;
+            if (8 * j < t.n && (own >> (2 * j + h) & 1u))
+              for (int q = 0; q < ranks; ++q) sum += cluster_load(smem_u32(red + 32 * i), q);
+            v[h][i & 15] = sum;
+          }
+        }
+      }
+      if (warp >= 2) finish<T, kGated>(a, t, 0, feat0, bias, v, res, base, own, lane);
+      if (ranks > 1) {
+        __syncwarp();
+        cluster_sync();  // no block leaves while another reads its partials
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (kPair) cluster_sync();  // no block leaves while the pair's products or arrivals are under way
+  tc_fence_after();
+  if (warp == 1) tmem_free<kPair>(tmem, S::kTmemCols);
+  if (threadIdx.x == 0 && *gave_up && a.status) atomicOr(a.status, LAPSUM_EXPERTS_TIMEOUT);
+}
+
+// ---- host -------------------------------------------------------------------------
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled g_encode = nullptr;
+
+// Tensor maps of 16-bit arrays, copied in boxes with 64 values along x in the
+// 128-byte swizzle; positions outside read as zero.  The swizzle does not look
+// at the type, so both 16-bit types are copied as bf16.
+cudaError_t encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                   const cuuint32_t* box) {
+  const cuuint32_t unit[5] = {1, 1, 1, 1, 1};
+  const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, unit,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+cudaError_t map_rows(CUtensorMap* m, const void* base, int64_t x, int64_t rows, int64_t stride, uint32_t box_y) {
+  const cuuint64_t dims[2] = {(cuuint64_t)x, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
+  const cuuint32_t box[2] = {64, box_y};
+  return encode(m, base, 2, dims, strides, box);
+}
+cudaError_t map_weights(CUtensorMap* m, const void* base, int64_t in, int64_t out, int experts, uint32_t box_y) {
+  const cuuint64_t dims[3] = {(cuuint64_t)in, (cuuint64_t)out, (cuuint64_t)experts};
+  const cuuint64_t strides[2] = {(cuuint64_t)in * 2, (cuuint64_t)in * 2 * (cuuint64_t)out};
+  const cuuint32_t box[3] = {64, box_y, 1};
+  return encode(m, base, 3, dims, strides, box);
+}
+// [expert][feature / 8][gate, up][feature % 8][in]: a box of 64 features
+cudaError_t map_gated(CUtensorMap* m, const void* base, int64_t in, int64_t out, int experts) {
+  const cuuint64_t row = (cuuint64_t)in * 2;
+  const cuuint64_t dims[5] = {(cuuint64_t)in, 8, 2, (cuuint64_t)out / 16, (cuuint64_t)experts};
+  const cuuint64_t strides[4] = {row, row * (cuuint64_t)(out / 2), row * 8, row * (cuuint64_t)out};
+  const cuuint32_t box[5] = {64, 8, 2, 8, 1};
+  return encode(m, base, 5, dims, strides, box);
+}
+
+template <typename T, int kMode, int kTok, bool kGated>
+cudaError_t allow_smem() {
+  return cudaFuncSetAttribute(k_product<T, kMode, kTok, kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Shape<kMode, kTok, kGated>::kSmem);
+}
+
+template <typename T, int kMode, int kTok, bool kGated>
+cudaError_t launch(const char* name, const CUtensorMap& mf, const CUtensorMap& mt, const Args& a, int64_t grid,
+                   int cluster, int tiles_grad_w, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Shape<kMode, kTok, kGated>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cluster;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  Launch guard(name, st);
+  return cudaLaunchKernelEx(&cfg, k_product<T, kMode, kTok, kGated>, mf, mt, a, tiles_grad_w);
+}
+
+// Forward and input gradient: the form by the mean number of rows of an expert
+// that can have any.
+template <typename T, int kMode, bool kGated>
+cudaError_t launch_rows(const char* name, const CUtensorMap& mf, const CUtensorMap& mt, const Args& a, int sms,
+                        cudaStream_t st) {
+  const int64_t live = std::min<int64_t>(a.experts, a.rows);
+  const int64_t mean = a.rows / std::max<int64_t>(1, live);
+  // tiles: at most one ragged one per expert, and one behind the last
+  auto bound = [&](int tok, int feat) {
+    return (std::min<int64_t>(a.experts + 1, a.rows) + a.rows / tok) * ((a.feat + feat - 1) / feat);
+  };
+  if (mean <= 32) {
+    const int64_t tiles = bound(32, Shape<kMode, 32, kGated>::kTileFeat);
+    const int chunks = (a.depth + kDepth - 1) / kDepth;
+    int ranks = 1;
+    while (ranks < 8 && tiles * ranks * 2 <= 2 * sms && chunks >= 8 * ranks) ranks *= 2;
+    return launch<T, kMode, 32, kGated>(name, mf, mt, a, tiles * ranks, ranks, 0, st);
+  }
+  if (mean <= 128)
+    return launch<T, kMode, 128, kGated>(
+        name, mf, mt, a, std::min<int64_t>(bound(128, Shape<kMode, 128, kGated>::kTileFeat), sms), 1, 0, st);
+  return launch<T, kMode, 256, kGated>(
+      name, mf, mt, a, 2 * std::min<int64_t>(bound(256, Shape<kMode, 256, kGated>::kTileFeat), sms / 2), 2, 0, st);
+}
+
+Args base_args(const Product& p) {
+  Args a{};
+  a.rows = p.rows;
+  a.experts = p.experts;
+  a.activation = p.activation;
+  a.offsets = p.offsets;
+  a.y = p.y;
+  a.y_stride = p.y_stride;
+  a.status = p.status;
+  return a;
+}
+
+template <typename T>
+cudaError_t init_as() {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult got = cudaDriverEntryPointSymbolNotFound;
+  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &got);
+  if (e != cudaSuccess) return e;
+  if (!fn || got != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
+  g_encode = reinterpret_cast<EncodeTiled>(fn);
+  for (cudaError_t r : {allow_smem<T, kForward, 32, false>(), allow_smem<T, kForward, 32, true>(),
+                        allow_smem<T, kForward, 128, false>(), allow_smem<T, kForward, 128, true>(),
+                        allow_smem<T, kForward, 256, false>(), allow_smem<T, kForward, 256, true>(),
+                        allow_smem<T, kGradX, 32, false>(), allow_smem<T, kGradX, 128, false>(),
+                        allow_smem<T, kGradX, 256, false>(), allow_smem<T, kGradW, 256, false>()})
+    if (r != cudaSuccess) return r;
+  return cudaSuccess;
+}
+
+template <typename T>
+cudaError_t fwd_as(const Product& p, int sms, cudaStream_t st) {
+  const bool gated = p.activation == LAPSUM_ACT_SWIGLU;
+  Args a = base_args(p);
+  a.feat = (int)(gated ? p.out / 2 : p.out);
+  a.depth = (int)p.in;
+  a.bias = p.bias;
+  a.residual = p.residual;
+  a.residual_stride = p.residual_stride;
+  a.preact = p.preact;
+  a.preact_stride = p.preact_stride;
+  CUtensorMap mf, mt;
+  cudaError_t e = gated ? map_gated(&mf, p.weight, p.in, p.out, p.experts)
+                        : map_weights(&mf, p.weight, p.in, p.out, p.experts, kLanes);
+  if (e == cudaSuccess) e = map_rows(&mt, p.x, p.in, p.rows, p.x_stride, kTokBox);
+  if (e != cudaSuccess) return e;
+  return gated ? launch_rows<T, kForward, true>("k_product_fwd", mf, mt, a, sms, st)
+               : launch_rows<T, kForward, false>("k_product_fwd", mf, mt, a, sms, st);
+}
+
+template <typename T>
+cudaError_t dx_as(const Product& p, int sms, cudaStream_t st) {
+  Args a = base_args(p);
+  a.feat = (int)p.in;
+  a.depth = (int)p.out;
+  CUtensorMap mf, mt;
+  cudaError_t e = map_weights(&mf, p.weight, p.in, p.out, p.experts, kDepth);
+  if (e == cudaSuccess) e = map_rows(&mt, p.grad_h, p.out, p.rows, p.grad_h_stride, kTokBox);
+  if (e != cudaSuccess) return e;
+  return launch_rows<T, kGradX, false>("k_product_dx", mf, mt, a, sms, st);
+}
+
+template <typename T>
+cudaError_t dweight_as(const Product& p, int sms, cudaStream_t st) {
+  Args a = base_args(p);
+  a.feat = (int)p.out;
+  a.cols = (int)p.in;
+  CUtensorMap mf, mt;
+  cudaError_t e = map_rows(&mf, p.grad_h, p.out, p.rows, p.grad_h_stride, kDepth);
+  if (e == cudaSuccess) e = map_rows(&mt, p.x, p.in, p.rows, p.x_stride, kDepth);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)p.experts * ((p.out + 255) / 256) * ((p.in + 255) / 256);
+  return launch<T, kGradW, 256, false>("k_product_dw", mf, mt, a, 2 * std::min<int64_t>(tiles, sms / 2), 2, (int)tiles, st);
+}
+
+}  // namespace
+}  // namespace lapsum

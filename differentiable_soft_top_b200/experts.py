@@ -409,7 +409,7 @@ def linear(x, weight, offsets=None, *, bias=None, activation: str | None = None,
         return _function("linear").apply(x, weight, bias, residual, offsets, act, status)
     w = _dense16(weight).view(experts, n, k)
     return _linear_fwd(_rows16(x), w, offsets, None if bias is None else bias.contiguous(), act,
-                       None if residual is None else _rows_of(residual), False, status)[0]
+                       None if residual is None else _rows16(residual), False, status)[0]
 
 
 def mlp(x, weights, chosen, w_in, w_out, *, b_in=None, b_out=None, activation: str | None = "swiglu", residual=None,
@@ -495,7 +495,7 @@ def _make_functions(torch):
             n, k = weight.shape[-2:]
             w2 = _dense16(weight).view(-1, n, k)
             y, h = _linear_fwd(x2, w2, offsets, None if bias is None else bias.contiguous(), act,
-                               None if residual is None else _rows_of(residual), act != 0, status)
+                               None if residual is None else _rows16(residual), act != 0, status)
             ctx.save_for_backward(x2, w2, offsets, h)
             ctx.act, ctx.weight_shape, ctx.status = act, weight.shape, status
             return y

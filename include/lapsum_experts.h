@@ -166,8 +166,9 @@ LAPSUM_API int lapsum_experts_combine_bwd(const void* grad, int dtype, int64_t t
  * and one rounding to the type.  Rows from offsets[experts] on get
  * residual_r (0 without a residual).
  *
- *   x           in   bf16 or fp16 [rows, in]; x_stride a multiple of 8, the
- *                    array 16-byte aligned
+ * x, residual, y and preact (and the gradients below) are 16-byte aligned with
+ * row strides that are multiples of 8.
+ *   x           in   bf16 or fp16 [rows, in]
  *   weight      in   [experts, out, in], contiguous, 16-byte aligned; in and
  *                    out multiples of 8 (out of 16 for LAPSUM_ACT_SWIGLU)
  *   offsets     in   int32 [experts + 1], ascending from 0; NULL with
@@ -201,8 +202,7 @@ LAPSUM_API int lapsum_experts_linear_act_bwd(const void* grad_y, int dtype, int6
                                              int64_t grad_h_stride, void* grad_bias, void* workspace,
                                              size_t workspace_bytes, void* stream);
 
-/* grad_x_r = W_e^T grad_h_r; rows from offsets[experts] on get 0.  grad_h_stride and
-   grad_h as x and x_stride in the forward. */
+/* grad_x_r = W_e^T grad_h_r; rows from offsets[experts] on get 0. */
 LAPSUM_API int lapsum_experts_linear_dx(const void* grad_h, int dtype, int64_t rows, int64_t out,
                                         int64_t grad_h_stride, const void* weight, int experts, int64_t in,
                                         const int32_t* offsets, void* grad_x, int64_t grad_x_stride,
