@@ -53,7 +53,7 @@ enum Mode { kForward, kGradX, kGradW };
 constexpr int kThreads = 192;
 constexpr int kDepth = 64;              // contraction per stage: one 128-byte line
 constexpr int kLanes = 128;             // accumulator lanes of a block
-constexpr int kTokBox = 32;             // tokens per copied box
+constexpr int kTokBox = 32;             // tokens per copied box of a ragged tile (a full one: one box)
 constexpr uint32_t kPolls = 1u << 22;   // polls of a bounded wait, about a second
 constexpr int kPitch = 80;              // bytes between staged rows of 64: conflict-free
 
@@ -434,11 +434,12 @@ __device__ __forceinline__ void fill(float (&v)[2][16], float x) {
   for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = x;
 }
 
-// map_f: the weights (kGradW: dH); map_t: the tokens' rows
+// map_f: the weights (kGradW: dH); map_t: the tokens' rows in small boxes,
+// map_full: in boxes of a full tile
 template <typename T, int kMode, int kTok, bool kGated>
 __global__ void __launch_bounds__(kThreads, Shape<kMode, kTok, kGated>::kSplit ? 2 : 1)
-    k_product(const __grid_constant__ CUtensorMap map_f, const __grid_constant__ CUtensorMap map_t, const Args a,
-              int tiles_grad_w) {
+    k_product(const __grid_constant__ CUtensorMap map_f, const __grid_constant__ CUtensorMap map_t,
+              const __grid_constant__ CUtensorMap map_full, const Args a, int tiles_grad_w) {
   using S = Shape<kMode, kTok, kGated>;
   constexpr int kStages = S::kStages;
   constexpr bool kPair = S::kPair;
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kMode, kTok, kGated>::kSplit ?
 
   if (warp == 0) {
     if (lane == 0) {
-      uint32_t it = 0;
+      uint32_t s = 0, ph = 0, used = 0;  // stage, its phase, stages filled (at most kStages)
       bool ok = true;
       for (int tile = first; ok && tile < tiles; tile += step) {
         const Tile t = tile_of<kMode, kTok, kGated>(a, table, tile, half);
@@ -518,10 +519,10 @@ __global__ void __launch_bounds__(kThreads, Shape<kMode, kTok, kGated>::kSplit ?
         share(t, c0, c1);
         width(t, n, n0, own);
         constexpr int kBox = kMode == kGradW ? 64 : kTokBox, kBoxBytes = kMode == kGradW ? 8192 : kTokBox * 128;
+        const bool whole = kMode != kGradW && own * 128 == S::kBBytes;  // one copy: issuing many is what limits
         const int boxes = (own + kBox - 1) / kBox;
         const uint32_t bytes = S::kABytes + boxes * kBoxBytes;
-        for (int c = c0; c < c1; ++c, ++it) {
-          const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
+        for (int c = c0; c < c1; ++c) {
           if (!wait_for(empty + s, ph ^ 1u, gave_up)) {
             ok = false;
             break;
@@ -542,94 +543,110 @@ __global__ void __launch_bounds__(kThreads, Shape<kMode, kTok, kGated>::kSplit ?
             tma_load_2d(sa, &map_f, t.f0, t.row0 + d, full + s);
             tma_load_2d(sa + 8192, &map_f, t.f0 + 64, t.row0 + d, full + s);
           }
-          for (int b = 0; b < boxes; ++b) {
+          if (whole) tma_load_2d(sb, &map_full, d, t.row0 + n0, full + s);
+          for (int b = whole ? boxes : 0; b < boxes; ++b) {
             if (kMode == kGradW)
               tma_load_2d(sb + b * kBoxBytes, &map_t, t.c0 + n0 + kBox * b, t.row0 + d, full + s);
             else
               tma_load_2d(sb + b * kBoxBytes, &map_t, d, t.row0 + n0 + kBox * b, full + s);
+          }
+          if (used < kStages) ++used;
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
           }
         }
       }
       // before the block ends, its copies in flight land (bounded); after a
       // normal end warp 1 has waited for every one of them
       if (!ok) {
-        for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0u; j < it; ++j)
-          mbar_wait_bounded(full + j % kStages, (j / kStages) & 1u, kPolls);
+        for (; used; --used) {
+          if (s == 0) ph ^= 1u;
+          s = s == 0 ? kStages - 1 : s - 1;
+          mbar_wait_bounded(full + s, ph, kPolls);
+        }
       }
     }
   } else if (warp == 1) {
-    uint32_t it = 0, done = 0;
-    bool ok = true;
-    for (int tile = first; ok && tile < tiles; tile += step) {
-      const Tile t = tile_of<kMode, kTok, kGated>(a, table, tile, half);
-      int c0, c1, n, n0, own;
-      share(t, c0, c1);
-      width(t, n, n0, own);
-      if (c0 == c1) continue;
-      const uint32_t buf = S::kSplit ? 0u : done & 1u;
-      if (half == 0) {
-        ok = __all_sync(0xffffffffu,
-                        wait_for(acc_empty + buf, ((S::kSplit ? done : done >> 1) & 1u) ^ 1u, gave_up));
-        if (!ok) break;
-        tc_fence_after();
-      }
-      const uint32_t acc = tmem + buf * kTok;
-      const uint32_t idesc =
-          instr_desc(std::is_same<T, __nv_bfloat16>::value, kMode != kForward, kMode == kGradW, kLanes * (kPair ? 2 : 1), n);
-      for (int c = c0; c < c1; ++c, ++it) {
-        const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
-        ok = __all_sync(0xffffffffu, wait_for(full + s, ph, gave_up));
-        if (!ok) break;
-        unsigned char* sa = ring + s * S::kStage;
-        unsigned char* sb = sa + S::kABytes;
-        if (kMode == kGradW) {
-          // lines of rows behind the expert's last one: zero in both operands
-          // (whatever they held, NaN included, must not reach the sums)
-          const int left = t.n - c * kDepth;
-          if (left < kDepth) {
-            const int lines = kDepth - left, blocks = 2 + (own + 63) / 64;
-            for (int i = lane; i < blocks * lines * 8; i += 32) {
-              const int line = i >> 3, blk = line / lines;
-              *reinterpret_cast<uint4*>(sa + blk * 8192 + (left + line - blk * lines) * 128 + (i & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
+    // One lane issues (and, in the second block of a pair, reports its stages);
+    // for weight gradients the warp stays together to zero ragged ends.
+    constexpr bool kWarp = kMode == kGradW;
+    if (kWarp || lane == 0) {
+      uint32_t s = 0, ph = 0, done = 0;
+      bool ok = true;
+      int tile = first;
+      Tile t = tile_of<kMode, kTok, kGated>(a, table, min(tile, max(tiles - 1, 0)), half);
+      for (; ok && tile < tiles; tile += step) {
+        const Tile cur = t;
+        int c0, c1, n, n0, own;
+        share(cur, c0, c1);
+        width(cur, n, n0, own);
+        if (c0 < c1) {
+          const uint32_t buf = S::kSplit ? 0u : done & 1u;
+          if (half == 0) ok = wait_for(acc_empty + buf, ((S::kSplit ? done : done >> 1) & 1u) ^ 1u, gave_up);
+          if (kWarp) ok = __all_sync(0xffffffffu, ok);
+          tc_fence_after();
+          const uint32_t acc = tmem + buf * kTok;
+          const uint32_t idesc = instr_desc(std::is_same<T, __nv_bfloat16>::value, kMode != kForward, kMode == kGradW,
+                                            kLanes * (kPair ? 2 : 1), n);
+          for (int c = c0; ok && c < c1; ++c) {
+            ok = wait_for(full + s, ph, gave_up);
+            if (kWarp) ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint32_t sa = smem_u32(ring) + s * S::kStage;
+            const int left = kMode == kGradW ? cur.n - c * kDepth : kDepth;
+            if (kMode == kGradW && left < kDepth) {
+              // lines of rows behind the expert's last one: zero in both operands
+              // (whatever they held, NaN included, must not reach the sums)
+              const int lines = kDepth - left, blocks = 2 + (own + 63) / 64;
+              for (int i = lane; i < blocks * lines * 8; i += 32) {
+                const int line = i >> 3, blk = line / lines;
+                sts16(sa + blk * 8192 + (left + line - blk * lines) * 128 + (i & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-        }
-        if (half != 0) {  // the first block issues for both
-          if (lane == 0) {
-            if (kMode == kGradW && t.n - c * kDepth < kDepth)
-              arrive_at<true>(peer_full + s, 0);
-            else
-              arrive_at<false>(peer_full + s, 0);
-          }
-          continue;
-        }
-        if (kPair) {
-          ok = __all_sync(0xffffffffu, wait_for(peer_full + s, ph, gave_up));
-          if (!ok) break;
-          if (kMode == kGradW && t.n - c * kDepth < kDepth) acquire_cluster();
-        }
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t da = operand_desc(smem_u32(sa), kMode == kForward ? 16u : 8192u);
-          const uint64_t db = operand_desc(smem_u32(sb), kMode == kGradW ? 8192u : 16u);
-          constexpr uint32_t kStepA = (kMode == kForward ? 32 : 2048) >> 4, kStepB = (kMode == kGradW ? 2048 : 32) >> 4;
+            if (half != 0) {  // the first block issues for both
+              if (lane == 0) {
+                if (left < kDepth)
+                  arrive_at<true>(peer_full + s, 0);
+                else
+                  arrive_at<false>(peer_full + s, 0);
+              }
+            } else {
+              if (kPair) {
+                ok = wait_for(peer_full + s, ph, gave_up);
+                if (kWarp) ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (left < kDepth) acquire_cluster();
+              }
+              if (lane == 0) {
+                tc_fence_after();
+                const uint64_t da = operand_desc(sa, kMode == kForward ? 16u : 8192u);
+                const uint64_t db = operand_desc(sa + S::kABytes, kMode == kGradW ? 8192u : 16u);
+                constexpr uint32_t kStepA = (kMode == kForward ? 32 : 2048) >> 4,
+                                   kStepB = (kMode == kGradW ? 2048 : 32) >> 4;
 #pragma unroll
-          for (uint32_t k = 0; k < kDepth / 16; ++k)
-            mma_f16<kPair>(acc, da + k * kStepA, db + k * kStepB, idesc, c != c0 || k != 0);
-          mma_commit<kPair>(empty + s);
-          if (c + 1 == c1) mma_commit<kPair>(acc_full + buf);
+                for (uint32_t k = 0; k < kDepth / 16; ++k)
+                  mma_f16<kPair>(acc, da + k * kStepA, db + k * kStepB, idesc, c != c0 || k != 0);
+                mma_commit<kPair>(empty + s);
+                if (c + 1 == c1) mma_commit<kPair>(acc_full + buf);
+              }
+            }
+            if (++s == kStages) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+          ++done;
         }
-        __syncwarp();
+        // the next tile is found while this one's products run
+        if (tile < tiles - step) t = tile_of<kMode, kTok, kGated>(a, table, tile + step, half);
       }
-      ++done;
-    }
-    if (!ok && half == 0) {  // the products in flight end before their tensor memory is freed
-      if (lane == 0) mma_commit<kPair>(drained);
-      __syncwarp();
-      mbar_wait_bounded(drained, 0u, kPolls);
+      if (!ok && half == 0) {  // the products in flight end before their tensor memory is freed
+        if (lane == 0) mma_commit<kPair>(drained);
+        mbar_wait_bounded(drained, 0u, kPolls);
+      }
     }
   } else if (!S::kSplit) {
     const int quarter = warp & 3;  // the lanes of tensor memory this warp may read
@@ -799,8 +816,8 @@ cudaError_t allow_smem() {
 }
 
 template <typename T, int kMode, int kTok, bool kGated>
-cudaError_t launch(const char* name, const CUtensorMap& mf, const CUtensorMap& mt, const Args& a, int64_t grid,
-                   int cluster, int tiles_grad_w, cudaStream_t st) {
+cudaError_t launch(const char* name, const CUtensorMap& mf, const CUtensorMap& mt, const CUtensorMap& full, const Args& a,
+                   int64_t grid, int cluster, int tiles_grad_w, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
@@ -814,32 +831,36 @@ cudaError_t launch(const char* name, const CUtensorMap& mf, const CUtensorMap& m
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
   Launch guard(name, st);
-  return cudaLaunchKernelEx(&cfg, k_product<T, kMode, kTok, kGated>, mf, mt, a, tiles_grad_w);
+  return cudaLaunchKernelEx(&cfg, k_product<T, kMode, kTok, kGated>, mf, mt, full, a, tiles_grad_w);
 }
 
 // Forward and input gradient: the form by the mean number of rows of an expert
 // that can have any.
 template <typename T, int kMode, bool kGated>
-cudaError_t launch_rows(const char* name, const CUtensorMap& mf, const CUtensorMap& mt, const Args& a, int sms,
+cudaError_t launch_rows(const char* name, const CUtensorMap& mf, const void* x, int64_t x_stride, const Args& a, int sms,
                         cudaStream_t st) {
+  CUtensorMap mt, full;
+  cudaError_t e = map_rows(&mt, x, a.depth, a.rows, x_stride, kTokBox);
   const int64_t live = std::min<int64_t>(a.experts, a.rows);
   const int64_t mean = a.rows / std::max<int64_t>(1, live);
   // tiles: at most one ragged one per expert, and one behind the last
   auto bound = [&](int tok, int feat) {
     return (std::min<int64_t>(a.experts + 1, a.rows) + a.rows / tok) * ((a.feat + feat - 1) / feat);
   };
+  if (e == cudaSuccess) e = map_rows(&full, x, a.depth, a.rows, x_stride, mean <= 32 ? 32 : 128);
+  if (e != cudaSuccess) return e;
   if (mean <= 32) {
     const int64_t tiles = bound(32, Shape<kMode, 32, kGated>::kTileFeat);
     const int chunks = (a.depth + kDepth - 1) / kDepth;
     int ranks = 1;
     while (ranks < 8 && tiles * ranks * 2 <= 2 * sms && chunks >= 8 * ranks) ranks *= 2;
-    return launch<T, kMode, 32, kGated>(name, mf, mt, a, tiles * ranks, ranks, 0, st);
+    return launch<T, kMode, 32, kGated>(name, mf, mt, full, a, tiles * ranks, ranks, 0, st);
   }
   if (mean <= 128)
     return launch<T, kMode, 128, kGated>(
-        name, mf, mt, a, std::min<int64_t>(bound(128, Shape<kMode, 128, kGated>::kTileFeat), sms), 1, 0, st);
+        name, mf, mt, full, a, std::min<int64_t>(bound(128, Shape<kMode, 128, kGated>::kTileFeat), sms), 1, 0, st);
   return launch<T, kMode, 256, kGated>(
-      name, mf, mt, a, 2 * std::min<int64_t>(bound(256, Shape<kMode, 256, kGated>::kTileFeat), sms / 2), 2, 0, st);
+      name, mf, mt, full, a, 2 * std::min<int64_t>(bound(256, Shape<kMode, 256, kGated>::kTileFeat), sms / 2), 2, 0, st);
 }
 
 Args base_args(const Product& p) {
@@ -882,13 +903,12 @@ cudaError_t fwd_as(const Product& p, int sms, cudaStream_t st) {
   a.residual_stride = p.residual_stride;
   a.preact = p.preact;
   a.preact_stride = p.preact_stride;
-  CUtensorMap mf, mt;
-  cudaError_t e = gated ? map_gated(&mf, p.weight, p.in, p.out, p.experts)
+  CUtensorMap mf;
+  const cudaError_t e = gated ? map_gated(&mf, p.weight, p.in, p.out, p.experts)
                         : map_weights(&mf, p.weight, p.in, p.out, p.experts, kLanes);
-  if (e == cudaSuccess) e = map_rows(&mt, p.x, p.in, p.rows, p.x_stride, kTokBox);
   if (e != cudaSuccess) return e;
-  return gated ? launch_rows<T, kForward, true>("k_product_fwd", mf, mt, a, sms, st)
-               : launch_rows<T, kForward, false>("k_product_fwd", mf, mt, a, sms, st);
+  return gated ? launch_rows<T, kForward, true>("k_product_fwd", mf, p.x, p.x_stride, a, sms, st)
+               : launch_rows<T, kForward, false>("k_product_fwd", mf, p.x, p.x_stride, a, sms, st);
 }
 
 template <typename T>
@@ -896,11 +916,10 @@ cudaError_t dx_as(const Product& p, int sms, cudaStream_t st) {
   Args a = base_args(p);
   a.feat = (int)p.in;
   a.depth = (int)p.out;
-  CUtensorMap mf, mt;
-  cudaError_t e = map_weights(&mf, p.weight, p.in, p.out, p.experts, kDepth);
-  if (e == cudaSuccess) e = map_rows(&mt, p.grad_h, p.out, p.rows, p.grad_h_stride, kTokBox);
+  CUtensorMap mf;
+  const cudaError_t e = map_weights(&mf, p.weight, p.in, p.out, p.experts, kDepth);
   if (e != cudaSuccess) return e;
-  return launch_rows<T, kGradX, false>("k_product_dx", mf, mt, a, sms, st);
+  return launch_rows<T, kGradX, false>("k_product_dx", mf, p.grad_h, p.grad_h_stride, a, sms, st);
 }
 
 template <typename T>
@@ -913,7 +932,7 @@ cudaError_t dweight_as(const Product& p, int sms, cudaStream_t st) {
   if (e == cudaSuccess) e = map_rows(&mt, p.x, p.in, p.rows, p.x_stride, kDepth);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)p.experts * ((p.out + 255) / 256) * ((p.in + 255) / 256);
-  return launch<T, kGradW, 256, false>("k_product_dw", mf, mt, a, 2 * std::min<int64_t>(tiles, sms / 2), 2, (int)tiles, st);
+  return launch<T, kGradW, 256, false>("k_product_dw", mf, mt, mt, a, 2 * std::min<int64_t>(tiles, sms / 2), 2, (int)tiles, st);
 }
 
 }  // namespace
