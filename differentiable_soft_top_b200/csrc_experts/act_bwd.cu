@@ -9,6 +9,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "activation.cuh"
 #include "experts.h"
 
 namespace lapsum {
@@ -61,17 +62,6 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8], int bf16) {
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-__device__ __forceinline__ float derivative(float h, int act) {
-  if (act == LAPSUM_ACT_RELU) return h > 0.0f ? 1.0f : 0.0f;
-  if (act == LAPSUM_ACT_SILU) {
-    const float s = 1.0f / (1.0f + __expf(-h));
-    return s * fmaf(h, 1.0f - s, 1.0f);
-  }
-  if (act == LAPSUM_ACT_GELU)  // Phi(h) + h phi(h)
-    return fmaf(0.5f, erff(h * 0.70710678f), 0.5f) + h * 0.39894228f * __expf(-0.5f * h * h);
-  return 1.0f;
 }
 
 // rows [lo, lo + n) of expert e, clamped into the array
@@ -129,33 +119,46 @@ __global__ void __launch_bounds__(kThreads) k_act_bwd(const ActArgs a, int max_t
     n = min(n - skip, kRows);
     float s0[8] = {}, s1[8] = {};
     if (f < a.width) {
-#pragma unroll 4
-      for (int r = lane8; r < n; r += 8) {
-        const int64_t row = row0 + r;
-        float g[8], h[8], u[8], d[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(a.gy + row * a.gy_stride + f)), a.bf16, g);
-        if (kGated) {
-          unpack8(__ldg(reinterpret_cast<const uint4*>(a.h + row * a.h_stride + f)), a.bf16, h);
-          unpack8(__ldg(reinterpret_cast<const uint4*>(a.h + row * a.h_stride + a.width + f)), a.bf16, u);
+      // four rows of a lane in flight
+      for (int r0 = lane8; r0 < n; r0 += 32) {
+        uint4 qg[4], qh[4], qu[kGated ? 4 : 1];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float s = 1.0f / (1.0f + __expf(-h[i]));
-            d[i] = g[i] * u[i] * s * fmaf(h[i], 1.0f - s, 1.0f);
-            u[i] = g[i] * h[i] * s;
-            s0[i] += d[i];
-            s1[i] += u[i];
+        for (int i = 0; i < 4; ++i) {
+          const int64_t row = row0 + min(r0 + 8 * i, n - 1);
+          qg[i] = __ldg(reinterpret_cast<const uint4*>(a.gy + row * a.gy_stride + f));
+          if (kGated || a.act != LAPSUM_ACT_NONE) qh[i] = __ldg(reinterpret_cast<const uint4*>(a.h + row * a.h_stride + f));
+          if constexpr (kGated) qu[i] = __ldg(reinterpret_cast<const uint4*>(a.h + row * a.h_stride + a.width + f));
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = r0 + 8 * q;
+          if (r >= n) break;
+          const int64_t row = row0 + r;
+          float g[8], h[8];
+          unpack8(qg[q], a.bf16, g);
+          if constexpr (kGated) {
+            float u[8], d[8];
+            unpack8(qh[q], a.bf16, h);
+            unpack8(qu[q], a.bf16, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float s = sigmoid_of(h[i]);
+              d[i] = g[i] * u[i] * s * fmaf(h[i], 1.0f - s, 1.0f);
+              u[i] = g[i] * h[i] * s;
+              s0[i] += d[i];
+              s1[i] += u[i];
+            }
+            *reinterpret_cast<uint4*>(a.gh + row * a.gh_stride + f) = pack8(d, a.bf16);
+            *reinterpret_cast<uint4*>(a.gh + row * a.gh_stride + a.width + f) = pack8(u, a.bf16);
+          } else {
+            if (a.act != LAPSUM_ACT_NONE) {
+              unpack8(qh[q], a.bf16, h);
+              differentiate(g, h, a.act);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s0[i] += g[i];
+            if (a.gh) *reinterpret_cast<uint4*>(a.gh + row * a.gh_stride + f) = pack8(g, a.bf16);
           }
-          *reinterpret_cast<uint4*>(a.gh + row * a.gh_stride + f) = pack8(d, a.bf16);
-          *reinterpret_cast<uint4*>(a.gh + row * a.gh_stride + a.width + f) = pack8(u, a.bf16);
-        } else {
-          if (a.act != LAPSUM_ACT_NONE) {
-            unpack8(__ldg(reinterpret_cast<const uint4*>(a.h + row * a.h_stride + f)), a.bf16, h);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] *= derivative(h[i], a.act);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s0[i] += g[i];
-          if (a.gh) *reinterpret_cast<uint4*>(a.gh + row * a.gh_stride + f) = pack8(g, a.bf16);
         }
       }
     }

@@ -204,19 +204,20 @@ __global__ void __launch_bounds__(kRowThreads) k_dispatch(const typename Elem<kD
     const bool some = (uint64_t)(int64_t)s < (uint64_t)slots;
     const P* src = reinterpret_cast<const P*>(x + (some ? s / k : 0) * x_stride);
     P* dst = reinterpret_cast<P*>(out + r * out_stride);
-    for (int p = p0 + lane; p < p1; p += 128) {
-      P v[4];
+    for (int p = p0 + lane; p < p1; p += 256) {
+      P v[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (p + 32 * i < p1) v[i] = some ? src[p + 32 * i] : zero_pack<kDtype, kVec>();
+      for (int i = 0; i < 8; ++i) v[i] = src[min(p + 32 * i, p1 - 1)];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (p + 32 * i < p1) dst[p + 32 * i] = v[i];
+      for (int i = 0; i < 8; ++i)
+        if (p + 32 * i < p1) dst[p + 32 * i] = some ? v[i] : zero_pack<kDtype, kVec>();
     }
   }
 }
 
-template <int kDtype, int kVec>
+// kRows rows x kPacks accesses of each are in flight per lane: enough of them
+// whatever k (k = 2 with one pack at a time reached 2.2 TB/s)
+template <int kDtype, int kVec, int kRows, int kPacks>
 __global__ void __launch_bounds__(kRowThreads)
     k_combine(const typename Elem<kDtype>::T* __restrict__ y, int64_t y_stride, const float* __restrict__ weights,
               const int32_t* __restrict__ rows, int k, int64_t all_rows,
@@ -235,42 +236,47 @@ __global__ void __launch_bounds__(kRowThreads)
       if ((uint64_t)(int64_t)row >= (uint64_t)all_rows) row = -1;
       wt = weights ? __ldg(weights + t * k + lane) : (row >= 0 ? 1.0f : 0.0f);
     }
-    for (int p = p0 + lane; p - lane < p1; p += 32) {
-      const bool on = p < p1;
-      float acc[kVec];
-      if (residual && on) {
-        const P v = reinterpret_cast<const P*>(residual + t * res_stride)[p];
+    for (int p = p0 + lane; p - lane < p1; p += 32 * kPacks) {
+      float acc[kPacks][kVec];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) acc[i] = Elem<kDtype>::get(v.v[i]);
-      } else {
+      for (int q = 0; q < kPacks; ++q) {
+        P v = zero_pack<kDtype, kVec>();
+        if (residual) v = reinterpret_cast<const P*>(residual + t * res_stride)[min(p + 32 * q, p1 - 1)];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) acc[i] = 0.0f;
+        for (int i = 0; i < kVec; ++i) acc[q][i] = Elem<kDtype>::get(v.v[i]);
       }
-      for (int j0 = 0; j0 < k; j0 += 8) {
-        P v[8];
-        float c[8];
+      for (int j0 = 0; j0 < k; j0 += kRows) {
+        P v[kRows][kPacks];
+        float c[kRows];
+        int r[kRows];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {  // up to 8 rows in flight
-          const int r = __shfl_sync(0xffffffffu, row, (j0 + j) & 31);
+        for (int j = 0; j < kRows; ++j) {
+          r[j] = __shfl_sync(0xffffffffu, row, (j0 + j) & 31);
           c[j] = __shfl_sync(0xffffffffu, wt, (j0 + j) & 31);
-          if (on && j0 + j < k && r >= 0)
-            v[j] = reinterpret_cast<const P*>(y + (int64_t)r * y_stride)[p];
-          else
-            v[j] = zero_pack<kDtype, kVec>();
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
           if (j0 + j < k) {
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) acc[i] = fmaf(c[j], Elem<kDtype>::get(v[j].v[i]), acc[i]);
+            for (int q = 0; q < kPacks; ++q)
+              v[j][q] = reinterpret_cast<const P*>(y + (int64_t)max(r[j], 0) * y_stride)[min(p + 32 * q, p1 - 1)];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+          if (j0 + j < k) {
+#pragma unroll
+            for (int q = 0; q < kPacks; ++q)
+#pragma unroll
+              for (int i = 0; i < kVec; ++i)  // a row that is not there adds w * 0
+                acc[q][i] = fmaf(c[j], r[j] >= 0 ? Elem<kDtype>::get(v[j][q].v[i]) : 0.0f, acc[q][i]);
           }
       }
-      if (on) {
-        P v;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) v.v[i] = Elem<kDtype>::put(acc[i]);
-        reinterpret_cast<P*>(out + t * out_stride)[p] = v;
-      }
+      for (int q = 0; q < kPacks; ++q)
+        if (p + 32 * q < p1) {
+          P v;
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) v.v[i] = Elem<kDtype>::put(acc[q][i]);
+          reinterpret_cast<P*>(out + t * out_stride)[p + 32 * q] = v;
+        }
     }
   }
 }
@@ -299,10 +305,10 @@ __global__ void __launch_bounds__(kRowThreads)
         P a[4], b[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (p + 32 * i < packs) {
-            a[i] = gp[p + 32 * i];
-            if (gw) b[i] = yp[p + 32 * i];
-          }
+          a[i] = gp[min(p + 32 * i, packs - 1)];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (gw) b[i] = yp[min(p + 32 * i, packs - 1)];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (p + 32 * i < packs) {
@@ -363,7 +369,8 @@ void combine_as(const void* y, int64_t tokens, int k, int64_t dim, int64_t y_str
                 cudaStream_t st) {
   using T = typename Elem<kDtype>::T;
   const Units u = make_units(tokens, dim / kVec, sms);
-  k_combine<kDtype, kVec><<<grid_of(u.rows * u.parts, sms), kRowThreads, 0, st>>>(
+  auto* kernel = k <= 2 ? k_combine<kDtype, kVec, 2, 4> : k <= 4 ? k_combine<kDtype, kVec, 4, 4> : k_combine<kDtype, kVec, 8, 2>;
+  kernel<<<grid_of(u.rows * u.parts, sms), kRowThreads, 0, st>>>(
       static_cast<const T*>(y), y_stride, weights, rows, k, tokens * k, static_cast<const T*>(residual), res_stride,
       static_cast<T*>(out), out_stride, u);
 }

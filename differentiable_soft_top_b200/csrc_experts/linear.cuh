@@ -42,6 +42,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "activation.cuh"
 #include "experts.h"
 #include "umma.cuh"
 
@@ -117,36 +118,6 @@ __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
 template <typename T>
 __device__ __forceinline__ float load1(const void* p, int64_t i) {
   return unpack2<T>((uint32_t)__ldg(static_cast<const uint16_t*>(p) + i)).x;
-}
-
-// ---- activations ----------------------------------------------------------------------
-__device__ __forceinline__ float sigmoid_of(float h) { return __fdividef(1.0f, 1.0f + __expf(-h)); }
-
-// The normal CDF by the rational approximation 7.1.26 of Abramowitz & Stegun
-// (|error| of erf <= 1.5e-7): 0.5 erfc(|h| / sqrt 2) = t P(t) exp(-h^2/2) / 2
-// with t = 1 / (1 + 0.3275911 |h| / sqrt 2).  The lower tail is not a difference.
-__device__ __forceinline__ float normal_cdf(float h) {
-  const float t = __fdividef(1.0f, fmaf(0.23164189f, fabsf(h), 1.0f));
-  float p = fmaf(t, 1.061405429f, -1.453152027f);
-  p = fmaf(t, p, 1.421413741f);
-  p = fmaf(t, p, -0.284496736f);
-  p = fmaf(t, p, 0.254829592f);
-  const float q = 0.5f * p * t * __expf(-0.5f * h * h);
-  return h < 0.0f ? q : 1.0f - q;
-}
-
-template <int N>
-__device__ __forceinline__ void activate(float (&v)[N], int act) {
-  if (act == LAPSUM_ACT_RELU) {
-#pragma unroll
-    for (int c = 0; c < N; ++c) v[c] = v[c] < 0.0f ? 0.0f : v[c];  // keeps NaN
-  } else if (act == LAPSUM_ACT_SILU) {
-#pragma unroll
-    for (int c = 0; c < N; ++c) v[c] *= sigmoid_of(v[c]);
-  } else if (act == LAPSUM_ACT_GELU) {
-#pragma unroll
-    for (int c = 0; c < N; ++c) v[c] *= normal_cdf(v[c]);
-  }
 }
 
 // ---- tiles ------------------------------------------------------------------------------

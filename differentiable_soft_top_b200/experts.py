@@ -23,7 +23,9 @@ import os
 import threading
 from dataclasses import dataclass
 
-from . import LAPSUM_ECUDA, LAPSUM_OK, LapsumError, _torch, status_string
+import torch
+
+from . import LAPSUM_ECUDA, LAPSUM_OK, LapsumError, status_string
 
 __all__ = ["route", "plan", "dispatch", "combine", "linear", "mlp", "Plan", "MAX_EXPERTS", "MAX_K", "MAX_GROUPS",
            "STATUS_TIMEOUT", "library_path"]
@@ -99,15 +101,29 @@ def _load():
 # ---------------------------------------------------------------------------
 # tensor marshalling
 # ---------------------------------------------------------------------------
-def _call(name, dev, *args):
-    """lapsum_experts_<name>(*args, stream) on the current stream of dev."""
-    torch = _torch()
-    fn = getattr(_load(), "lapsum_experts_" + name)
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+_F32, _BF16, _F16, _I32 = torch.float32, torch.bfloat16, torch.float16, torch.int32
+_DTYPES = {_F32: 0, _BF16: 1, _F16: 2}
+_fns: dict = {}  # entry points by name
+
+
+def _stream_of(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same handle without the Stream object around it (3 us of the 5 us a call takes)
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
+
+
+def _call(name, index, *args):
+    """lapsum_experts_<name>(*args, stream) on the current stream of device `index`."""
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(_load(), "lapsum_experts_" + name)
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _stream_of(index))
     else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(index):
+            rc = fn(*args, _stream_of(index))
     if rc != LAPSUM_OK:
         raise ExpertsError(rc, "lapsum_experts_" + name)
 
@@ -117,16 +133,14 @@ def _ptr(t):
 
 
 def _dtype(t, name, *, half_only=False):
-    torch = _torch()
-    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(t.dtype)
+    code = _DTYPES.get(t.dtype)
     if code is None or (half_only and code == 0):
         raise TypeError(f"{name} must be {'' if half_only else 'float32, '}bfloat16 or float16, got {t.dtype}")
     return code
 
 
 def _cuda(t, name, dim=None, dev=None):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise TypeError(f"{name} must be a CUDA tensor (this library has no CPU path)")
     if dim is not None and t.dim() != dim:
         raise ValueError(f"{name} must be {dim}-D, got shape {tuple(t.shape)}")
@@ -137,6 +151,8 @@ def _cuda(t, name, dim=None, dev=None):
 
 def _rows_of(t):
     """t (2-D) with unit stride along its rows and rows that do not overlap."""
+    if t.is_contiguous():
+        return t
     r, n = t.shape
     if (t.stride(1) == 1 or n == 1) and (t.stride(0) >= n or r == 1):
         return t
@@ -153,7 +169,7 @@ def _rows16(t):
     copies need them."""
     t = _rows_of(t)
     if t.data_ptr() % 16 or (t.shape[0] > 1 and t.stride(0) % 8):
-        t = t.clone(memory_format=_torch().contiguous_format)
+        t = t.clone(memory_format=torch.contiguous_format)
     return t
 
 
@@ -163,8 +179,7 @@ def _dense16(t):
 
 
 def _index(t, name, dev):
-    torch = _torch()
-    if t.dtype != torch.int32:
+    if t.dtype != _I32:
         raise TypeError(f"{name} must be int32, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}, got {t.device}")
@@ -177,25 +192,33 @@ _functions: dict = {}
 def _function(name):
     """The autograd.Function of an operator, made on first use."""
     if not _functions:
-        _make_functions(_torch())
+        _make_functions()
     return _functions[name]
 
 
 def _tracked(*ts):
-    torch = _torch()
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts)
+    if torch.is_grad_enabled():
+        for t in ts:
+            if t is not None and t.requires_grad:
+                return True
+    return False
+
+
+def _once():
+    """The gradients' own gradients are not there."""
+    if torch.is_grad_enabled():
+        raise RuntimeError("the expert operators cannot be differentiated twice (create_graph=True)")
 
 
 # ---------------------------------------------------------------------------
 # operators
 # ---------------------------------------------------------------------------
 def _route_fwd(scores, k, score, bias, groups, kept, top, renormalize, scale):
-    torch = _torch()
     t, e = scores.shape
-    w = torch.empty((t, k), dtype=torch.float32, device=scores.device)
-    chosen = torch.empty((t, k), dtype=torch.int32, device=scores.device)
+    w = torch.empty((t, k), dtype=_F32, device=scores.device)
+    chosen = torch.empty((t, k), dtype=_I32, device=scores.device)
     if t:
-        _call("route_fwd", scores.device, scores.data_ptr(), _dtype(scores, "scores"), t, e, _stride(scores), k, score,
+        _call("route_fwd", scores.get_device(), scores.data_ptr(), _dtype(scores, "scores"), t, e, _stride(scores), k, score,
               _ptr(bias), groups, kept, top, int(renormalize), scale, w.data_ptr(), chosen.data_ptr())
     return w, chosen
 
@@ -217,7 +240,6 @@ def route(scores, k: int, *, score: str = "softmax", bias=None, groups: int = 1,
     A score or bias of -inf masks an expert.  Where fewer than k are left the
     places get expert -1 and weight 0; a token with a NaN or +inf (unmasked)
     gets expert -1 and weight NaN."""
-    torch = _torch()
     _cuda(scores, "scores", 2)
     _dtype(scores, "scores")
     t, e = scores.shape
@@ -236,7 +258,7 @@ def route(scores, k: int, *, score: str = "softmax", bias=None, groups: int = 1,
         raise ValueError(f"scale must be finite and positive, got {scale}")
     if bias is not None:
         _cuda(bias, "bias", 1, scores.device)
-        if bias.dtype != torch.float32 or bias.shape[0] != e:
+        if bias.dtype != _F32 or bias.shape[0] != e:
             raise ValueError(f"bias must be float32 [{e}], got {bias.dtype} {tuple(bias.shape)}")
         bias = bias.detach().contiguous()
     args = (k, _SCORES[score], bias, groups, kept, group_top, bool(renormalize), scale)
@@ -257,7 +279,6 @@ def plan(chosen, experts: int) -> Plan:
     """Plan of the exchange for chosen [tokens, k] (int32, from route()); a
     place whose expert is not in 0..experts-1 is dropped.  The rows of one
     expert are in the order of their slots."""
-    torch = _torch()
     _cuda(chosen, "chosen", 2)
     experts = int(experts)
     if not 1 <= experts <= MAX_EXPERTS:
@@ -267,14 +288,14 @@ def plan(chosen, experts: int) -> Plan:
     chosen = _index(chosen, "chosen", chosen.device)
     n, dev = chosen.numel(), chosen.device
     if n == 0:
-        return Plan(torch.zeros(experts + 1, dtype=torch.int32, device=dev), torch.empty_like(chosen),
-                    torch.empty(0, dtype=torch.int32, device=dev))
-    offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
+        return Plan(torch.zeros(experts + 1, dtype=_I32, device=dev), torch.empty_like(chosen),
+                    torch.empty(0, dtype=_I32, device=dev))
+    offsets = torch.empty(experts + 1, dtype=_I32, device=dev)
     rows = torch.empty_like(chosen)
-    slots = torch.empty(n, dtype=torch.int32, device=dev)
+    slots = torch.empty(n, dtype=_I32, device=dev)
     need = int(_load().lapsum_experts_plan_workspace_size(n, experts))
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _call("plan", dev, chosen.data_ptr(), n, experts, offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), _ptr(ws),
+    _call("plan", chosen.get_device(), chosen.data_ptr(), n, experts, offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), _ptr(ws),
           need)
     return Plan(offsets, rows, slots)
 
@@ -288,10 +309,9 @@ def _check_plan(p, dev):
 
 
 def _dispatch(x, slots, t, k):
-    torch = _torch()
     out = torch.empty((t * k, x.shape[1]), dtype=x.dtype, device=x.device)
     if out.numel():
-        _call("dispatch", x.device, x.data_ptr(), _dtype(x, "x"), t, k, x.shape[1], _stride(x), slots.data_ptr(),
+        _call("dispatch", x.get_device(), x.data_ptr(), _dtype(x, "x"), t, k, x.shape[1], _stride(x), slots.data_ptr(),
               out.data_ptr(), x.shape[1])
     return out
 
@@ -310,11 +330,10 @@ def dispatch(x, p: Plan):
 
 
 def _combine(y, weights, rows, residual):
-    torch = _torch()
     (t, k), dim = rows.shape, y.shape[1]
     out = torch.empty((t, dim), dtype=y.dtype, device=y.device)
     if out.numel():
-        _call("combine", y.device, y.data_ptr(), _dtype(y, "y"), t, k, dim, _stride(y), _ptr(weights), rows.data_ptr(),
+        _call("combine", y.get_device(), y.data_ptr(), _dtype(y, "y"), t, k, dim, _stride(y), _ptr(weights), rows.data_ptr(),
               _ptr(residual), _stride(residual) if residual is not None else 0, out.data_ptr(), dim)
     return out
 
@@ -323,7 +342,6 @@ def combine(y, weights, p: Plan, *, residual=None):
     """Expert order to token order: out[t] = residual[t] + sum_j weights[t, j]
     y[rows[t, j]], summed in fp32 in the order of j.  y [tokens * k, dim] (fp32,
     bf16, fp16), weights fp32 [tokens, k], residual [tokens, dim] of y's type."""
-    torch = _torch()
     _cuda(y, "y", 2)
     _dtype(y, "y")
     dev = y.device
@@ -331,7 +349,7 @@ def combine(y, weights, p: Plan, *, residual=None):
     if y.shape[0] != t * k:
         raise ValueError(f"y must have the plan's {t * k} rows, got {y.shape[0]}")
     _cuda(weights, "weights", 2, dev)
-    if weights.dtype != torch.float32 or tuple(weights.shape) != (t, k):
+    if weights.dtype != _F32 or tuple(weights.shape) != (t, k):
         raise ValueError(f"weights must be float32 [{t}, {k}], got {weights.dtype} {tuple(weights.shape)}")
     if residual is not None:
         _cuda(residual, "residual", 2, dev)
@@ -345,13 +363,12 @@ def combine(y, weights, p: Plan, *, residual=None):
 
 def _linear_fwd(x, weight, offsets, bias, act, residual, keep, status):
     """y and, with keep, the pre-activation; x, weight laid out for the kernels."""
-    torch = _torch()
     r, (experts, n, _) = x.shape[0], weight.shape
     width = n // 2 if act == 4 else n
     y = torch.empty((r, width), dtype=x.dtype, device=x.device)
     h = torch.empty((r, n), dtype=x.dtype, device=x.device) if keep else None
     if r:
-        _call("linear_fwd", x.device, x.data_ptr(), _dtype(x, "x"), r, x.shape[1], _stride(x), weight.data_ptr(), experts,
+        _call("linear_fwd", x.get_device(), x.data_ptr(), _dtype(x, "x"), r, x.shape[1], _stride(x), weight.data_ptr(), experts,
               n, _ptr(offsets), _ptr(bias), act, _ptr(residual), _stride(residual) if residual is not None else 0,
               y.data_ptr(), width, _ptr(h), n, _ptr(status))
     return y, h
@@ -370,7 +387,6 @@ def linear(x, weight, offsets=None, *, bias=None, activation: str | None = None,
     result half as wide).  Rows from offsets[-1] on get the residual (0).
 
     status: an int32 [1] tensor into which STATUS_* bits are or'ed (optional)."""
-    torch = _torch()
     _cuda(x, "x", 2)
     _dtype(x, "x", half_only=True)
     dev = x.device
@@ -403,7 +419,7 @@ def linear(x, weight, offsets=None, *, bias=None, activation: str | None = None,
         if residual.dtype != x.dtype or tuple(residual.shape) != (x.shape[0], width):
             raise ValueError(f"residual must be {x.dtype} [{x.shape[0]}, {width}], got {residual.dtype} "
                              f"{tuple(residual.shape)}")
-    if status is not None and (_cuda(status, "status", None, dev).dtype != torch.int32 or status.numel() < 1):
+    if status is not None and (_cuda(status, "status", None, dev).dtype != _I32 or status.numel() < 1):
         raise TypeError("status must be an int32 tensor")
     if _tracked(x, weight, bias, residual):
         return _function("linear").apply(x, weight, bias, residual, offsets, act, status)
@@ -427,9 +443,7 @@ def mlp(x, weights, chosen, w_in, w_out, *, b_in=None, b_out=None, activation: s
 # ---------------------------------------------------------------------------
 # gradients
 # ---------------------------------------------------------------------------
-def _make_functions(torch):
-    from torch.autograd.function import once_differentiable
-
+def _make_functions():
     class Route(torch.autograd.Function):
         @staticmethod
         def forward(ctx, scores, k, score, bias, groups, kept, top, renormalize, scale):
@@ -441,15 +455,15 @@ def _make_functions(torch):
             return w, chosen
 
         @staticmethod
-        @once_differentiable
         def backward(ctx, gw, _):
+            _once()
             x, bias, w, chosen = ctx.saved_tensors
             k, score, renormalize, scale = ctx.rule
             t, e = x.shape
             grad = torch.empty((t, e), dtype=x.dtype, device=x.device)
             if t:
                 gw = gw.contiguous()
-                _call("route_bwd", x.device, x.data_ptr(), _dtype(x, "scores"), t, e, _stride(x), k, score, _ptr(bias),
+                _call("route_bwd", x.get_device(), x.data_ptr(), _dtype(x, "scores"), t, e, _stride(x), k, score, _ptr(bias),
                       int(renormalize), scale, chosen.data_ptr(), w.data_ptr(), gw.data_ptr(), grad.data_ptr(), e)
             return (grad,) + (None,) * 8
 
@@ -460,8 +474,8 @@ def _make_functions(torch):
             return _dispatch(_rows_of(x), slots, *rows.shape)
 
         @staticmethod
-        @once_differentiable
         def backward(ctx, g):
+            _once()
             (rows,) = ctx.saved_tensors
             return _combine(_rows_of(g), None, rows, None), None, None
 
@@ -473,8 +487,8 @@ def _make_functions(torch):
             return _combine(y2, w2, rows, None if residual is None else _rows_of(residual))
 
         @staticmethod
-        @once_differentiable
         def backward(ctx, g):
+            _once()
             y, w, rows, slots = ctx.saved_tensors
             need_y, need_w, need_r = ctx.needs_input_grad[:3]
             (t, k), dim = rows.shape, y.shape[1]
@@ -482,7 +496,7 @@ def _make_functions(torch):
             gw = torch.empty_like(w) if need_w else None
             if (need_y or need_w) and t * dim:
                 gg = _rows_of(g)
-                _call("combine_bwd", y.device, gg.data_ptr(), _dtype(y, "y"), t, k, dim, _stride(gg), y.data_ptr(),
+                _call("combine_bwd", y.get_device(), gg.data_ptr(), _dtype(y, "y"), t, k, dim, _stride(gg), y.data_ptr(),
                       _stride(y), w.data_ptr(), rows.data_ptr(), slots.data_ptr(), _ptr(gy), dim, _ptr(gw))
             elif gw is not None:
                 gw.zero_()
@@ -501,13 +515,13 @@ def _make_functions(torch):
             return y
 
         @staticmethod
-        @once_differentiable
         def backward(ctx, g):
+            _once()
             x, w, offsets, h = ctx.saved_tensors
             status = ctx.status
             need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
             experts, n, k = w.shape
-            r, act, dev, dt = x.shape[0], ctx.act, x.device, _dtype(x, "x")
+            r, act, dev, dt, index = x.shape[0], ctx.act, x.device, _dtype(x, "x"), x.get_device()
             gb = torch.empty(ctx.weight_shape[:-1], dtype=x.dtype, device=dev) if need_b else None
             gx = torch.empty((r, k), dtype=x.dtype, device=dev) if need_x else None
             gwt = torch.empty(ctx.weight_shape, dtype=x.dtype, device=dev) if need_w else None
@@ -523,14 +537,14 @@ def _make_functions(torch):
                     gh = torch.empty((r, n), dtype=x.dtype, device=dev) if act else None
                     need = int(_load().lapsum_experts_linear_act_workspace_size(r, experts, n)) if need_b else 0
                     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-                    _call("linear_act_bwd", dev, gy.data_ptr(), dt, r, n, _stride(gy), _ptr(h), n, experts, _ptr(offsets),
+                    _call("linear_act_bwd", index, gy.data_ptr(), dt, r, n, _stride(gy), _ptr(h), n, experts, _ptr(offsets),
                           act, _ptr(gh), n, _ptr(gb), _ptr(ws), need)
                     gh = gh if act else gy
                 if need_x:
-                    _call("linear_dx", dev, gh.data_ptr(), dt, r, n, _stride(gh), w.data_ptr(), experts, k, _ptr(offsets),
+                    _call("linear_dx", index, gh.data_ptr(), dt, r, n, _stride(gh), w.data_ptr(), experts, k, _ptr(offsets),
                           gx.data_ptr(), k, _ptr(status))
                 if need_w:
-                    _call("linear_dweight", dev, gh.data_ptr(), dt, r, n, _stride(gh), x.data_ptr(), k, _stride(x), experts,
+                    _call("linear_dweight", index, gh.data_ptr(), dt, r, n, _stride(gh), x.data_ptr(), k, _stride(x), experts,
                           _ptr(offsets), gwt.data_ptr(), _ptr(status))
             return gx, gwt, gb, g if need_r else None, None, None, None
 
