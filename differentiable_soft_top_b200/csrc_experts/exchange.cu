@@ -215,67 +215,77 @@ __global__ void __launch_bounds__(kRowThreads) k_dispatch(const typename Elem<kD
   }
 }
 
-// kRows rows x kPacks accesses of each are in flight per lane: enough of them
-// whatever k (k = 2 with one pack at a time reached 2.2 TB/s)
+// `per_row` threads (32 .. 256, a power of two) take a token; each keeps kPacks
+// accesses of kRows rows in flight, 8 in all whatever k.  A row is read in pieces
+// as long as the block allows: DRAM likes 4 KB of a row at once (a warp per
+// token, which came back for 512 bytes of each row at a time, took 1.3 to 2
+// times as long).  The next token's row numbers are read ahead.
 template <int kDtype, int kVec, int kRows, int kPacks>
 __global__ void __launch_bounds__(kRowThreads)
     k_combine(const typename Elem<kDtype>::T* __restrict__ y, int64_t y_stride, const float* __restrict__ weights,
-              const int32_t* __restrict__ rows, int k, int64_t all_rows,
+              const int32_t* __restrict__ rows, int64_t tokens, int k, int64_t all_rows,
               const typename Elem<kDtype>::T* __restrict__ residual, int64_t res_stride,
-              typename Elem<kDtype>::T* __restrict__ out, int64_t out_stride, Units u) {
+              typename Elem<kDtype>::T* __restrict__ out, int64_t out_stride, int packs, int per_row) {
   using P = Pack<kDtype, kVec>;
-  const int lane = threadIdx.x & 31;
-  const int64_t nwarp = (int64_t)gridDim.x * (kRowThreads / 32);
-  for (int64_t w = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); w < u.rows * u.parts; w += nwarp) {
-    const int64_t t = w / u.parts;
-    const int p0 = (int)(w - t * u.parts) * u.per, p1 = min(u.packs, p0 + u.per);
-    int row = -1;
-    float wt = 0.0f;
-    if (lane < k) {
-      row = __ldg(rows + t * k + lane);
-      if ((uint64_t)(int64_t)row >= (uint64_t)all_rows) row = -1;
-      wt = weights ? __ldg(weights + t * k + lane) : (row >= 0 ? 1.0f : 0.0f);
+  const int in_block = kRowThreads / per_row;
+  const int64_t step = (int64_t)gridDim.x * in_block;
+  int64_t t = (int64_t)blockIdx.x * in_block + threadIdx.x / per_row;
+  auto look = [&](int64_t tok, int j0, int (&r)[kRows], float (&c)[kRows]) {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int64_t at = tok * k + min(j0 + j, k - 1);
+      r[j] = __ldg(rows + at);
+      c[j] = weights ? __ldg(weights + at) : 1.0f;
     }
-    for (int p = p0 + lane; p - lane < p1; p += 32 * kPacks) {
+  };
+  int r[kRows], r1[kRows];
+  float c[kRows], c1[kRows];
+  if (t < tokens) look(t, 0, r1, c1);
+  for (; t < tokens; t += step) {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      r[j] = r1[j];
+      c[j] = c1[j];
+    }
+    if (t + step < tokens) look(t + step, 0, r1, c1);
+    for (int p = threadIdx.x % per_row; p < packs; p += per_row * kPacks) {
       float acc[kPacks][kVec];
 #pragma unroll
       for (int q = 0; q < kPacks; ++q) {
         P v = zero_pack<kDtype, kVec>();
-        if (residual) v = reinterpret_cast<const P*>(residual + t * res_stride)[min(p + 32 * q, p1 - 1)];
+        if (residual) v = reinterpret_cast<const P*>(residual + t * res_stride)[min(p + q * per_row, packs - 1)];
 #pragma unroll
         for (int i = 0; i < kVec; ++i) acc[q][i] = Elem<kDtype>::get(v.v[i]);
       }
       for (int j0 = 0; j0 < k; j0 += kRows) {
+        if (k > kRows) look(t, j0, r, c);
         P v[kRows][kPacks];
-        float c[kRows];
-        int r[kRows];
-#pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-          r[j] = __shfl_sync(0xffffffffu, row, (j0 + j) & 31);
-          c[j] = __shfl_sync(0xffffffffu, wt, (j0 + j) & 31);
-          if (j0 + j < k) {
-#pragma unroll
-            for (int q = 0; q < kPacks; ++q)
-              v[j][q] = reinterpret_cast<const P*>(y + (int64_t)max(r[j], 0) * y_stride)[min(p + 32 * q, p1 - 1)];
-          }
-        }
 #pragma unroll
         for (int j = 0; j < kRows; ++j)
           if (j0 + j < k) {
+            const bool some = (uint64_t)(int64_t)r[j] < (uint64_t)all_rows;
+            const P* src = reinterpret_cast<const P*>(y + (some ? (int64_t)r[j] : 0) * y_stride);
+#pragma unroll
+            for (int q = 0; q < kPacks; ++q) v[j][q] = src[min(p + q * per_row, packs - 1)];
+          }
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+          if (j0 + j < k) {
+            const bool some = (uint64_t)(int64_t)r[j] < (uint64_t)all_rows;
 #pragma unroll
             for (int q = 0; q < kPacks; ++q)
 #pragma unroll
               for (int i = 0; i < kVec; ++i)  // a row that is not there adds w * 0
-                acc[q][i] = fmaf(c[j], r[j] >= 0 ? Elem<kDtype>::get(v[j][q].v[i]) : 0.0f, acc[q][i]);
+                acc[q][i] = fmaf(c[j], some ? Elem<kDtype>::get(v[j][q].v[i]) : 0.0f, acc[q][i]);
           }
       }
 #pragma unroll
       for (int q = 0; q < kPacks; ++q)
-        if (p + 32 * q < p1) {
+        if (p + q * per_row < packs) {
           P v;
 #pragma unroll
           for (int i = 0; i < kVec; ++i) v.v[i] = Elem<kDtype>::put(acc[q][i]);
-          reinterpret_cast<P*>(out + t * out_stride)[p + 32 * q] = v;
+          reinterpret_cast<P*>(out + t * out_stride)[p + q * per_row] = v;
         }
     }
   }
@@ -368,11 +378,14 @@ void combine_as(const void* y, int64_t tokens, int k, int64_t dim, int64_t y_str
                 const int32_t* rows, const void* residual, int64_t res_stride, void* out, int64_t out_stride, int sms,
                 cudaStream_t st) {
   using T = typename Elem<kDtype>::T;
-  const Units u = make_units(tokens, dim / kVec, sms);
-  auto* kernel = k <= 2 ? k_combine<kDtype, kVec, 2, 4> : k <= 4 ? k_combine<kDtype, kVec, 4, 4> : k_combine<kDtype, kVec, 8, 2>;
-  kernel<<<grid_of(u.rows * u.parts, sms), kRowThreads, 0, st>>>(
-      static_cast<const T*>(y), y_stride, weights, rows, k, tokens * k, static_cast<const T*>(residual), res_stride,
-      static_cast<T*>(out), out_stride, u);
+  const int packs = (int)(dim / kVec), each = k <= 2 ? 4 : k <= 4 ? 2 : 1;
+  int per_row = 32;
+  while (per_row < kRowThreads && per_row * each < packs) per_row *= 2;
+  const int64_t blocks = (tokens + kRowThreads / per_row - 1) / (kRowThreads / per_row);
+  auto* kernel = k <= 2 ? k_combine<kDtype, kVec, 2, 4> : k <= 4 ? k_combine<kDtype, kVec, 4, 2> : k_combine<kDtype, kVec, 8, 1>;
+  kernel<<<(unsigned)std::min<int64_t>(blocks, (int64_t)sms * 8), kRowThreads, 0, st>>>(
+      static_cast<const T*>(y), y_stride, weights, rows, tokens, k, tokens * k, static_cast<const T*>(residual), res_stride,
+      static_cast<T*>(out), out_stride, packs, per_row);
 }
 template <int kDtype, int kVec>
 void combine_bwd_as(const void* grad, int64_t tokens, int k, int64_t dim, int64_t grad_stride, const void* y,
