@@ -122,7 +122,7 @@ int lapsum_experts_route_fwd(const void* scores, int dtype, int64_t tokens, int 
     return LAPSUM_EINVAL;
   if (!device_sms()) return LAPSUM_ECUDA;
   RouteFwd a{scores, dtype, tokens, row_stride, experts, k, score, bias, groups, groups_kept, group_top,
-             renormalize != 0, scale, weights, chosen};
+             renormalize != 0, scale, weights, chosen, false};
   return done(launch_route_fwd(a, (cudaStream_t)stream));
 }
 
@@ -143,7 +143,7 @@ int lapsum_experts_route_bwd(const void* scores, int dtype, int64_t tokens, int 
     return LAPSUM_EINVAL;
   if (!device_sms()) return LAPSUM_ECUDA;
   RouteBwd a{scores, dtype, tokens, row_stride, experts, k, score, bias, renormalize != 0, scale, chosen, weights,
-             grad_weights, grad_scores, grad_stride};
+             grad_weights, grad_scores, grad_stride, false, false};
   return done(launch_route_bwd(a, (cudaStream_t)stream));
 }
 
