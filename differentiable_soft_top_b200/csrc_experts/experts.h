@@ -20,9 +20,9 @@ struct RouteFwd {
   float scale;
   float* weights;
   int32_t* chosen;
-  bool vec;  // set by the launcher
+  bool vec, bias_vec;  // set by the launcher
 };
-cudaError_t launch_route_fwd(RouteFwd a, cudaStream_t st);
+cudaError_t launch_route_fwd(RouteFwd a, int sms, cudaStream_t st);
 
 struct RouteBwd {
   const void* scores;
@@ -37,9 +37,9 @@ struct RouteBwd {
   const float* grad_weights;
   void* grad;
   int64_t grad_stride;
-  bool vec, grad_vec;  // set by the launcher
+  bool vec, bias_vec, grad_vec;  // set by the launcher
 };
-cudaError_t launch_route_bwd(RouteBwd a, cudaStream_t st);
+cudaError_t launch_route_bwd(RouteBwd a, int sms, cudaStream_t st);
 
 size_t plan_workspace(int64_t slots, int experts);
 cudaError_t launch_plan(const int32_t* chosen, int64_t slots, int experts, int32_t* offsets, int32_t* rows,

@@ -7,11 +7,12 @@
 // once.  The floor is the scores' bytes; what bounds it is the issue of the k
 // rounds, some 40 instructions each.
 //
-// Equal results whatever the rounding: without a bias and without sums of two
-// keys the order of the keys is the order of the scores, which are compared as
-// they are.  Otherwise fp32 keys decide only when neighbours in the order lie
-// further apart than the fp32 error can reach; a token where they do not is
-// done again with fp64 keys (about 1 in 1000 at 256 experts).
+// Equal results whatever the rounding: fp32 keys, their last 5 bits replaced by
+// the place in the lane, decide only when neighbours in the order lie further
+// apart than that and the fp32 error can reach, or are truly equal; a token
+// where they do not is done again with fp64 keys (less than 1 in 100 at 256
+// experts).  Without a bias and without sums of two keys the order of the keys
+// is the order of the scores, which 16-bit scores show exactly.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -54,8 +55,9 @@ __device__ __forceinline__ K warp_sum(K v) {
 
 // integers in the order of the keys; 0 is below every key
 __device__ __forceinline__ uint32_t ordered(float f) {
-  uint32_t u = __float_as_uint(f);
-  u = u == 0x80000000u ? 0u : u;  // -0 as +0 (an addition would flush subnormals)
+  float z;  // -0 as +0; subnormals stay (no .ftz)
+  asm("add.f32 %0, %1, 0f00000000;" : "=f"(z) : "f"(f));
+  const uint32_t u = __float_as_uint(z);
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ uint64_t ordered(double f) {
@@ -104,6 +106,7 @@ struct Keys {
   int64_t at;         // the token's first score
   const float* bias;
   float bias_max;
+  float top, scale;   // softmax: the largest score and 1 / sum exp(score - top)
 };
 
 // (a, b) = the two highest of a >= b and c >= d
@@ -121,123 +124,230 @@ __device__ __forceinline__ uint32_t shuffle_xor<uint32_t>(uint32_t v, int d) {
   return __shfl_xor_sync(kAll, v, d);
 }
 
-// Lane j < k gets the token's j-th choice (or -1).  l: this lane's scores, -inf
-// where masked; b: its biases.  picked: k + 1 pairs (expert, key) in shared
-// memory.  Returns whether the choice is certain at the precision of K (always,
-// for fp64 and for raw keys).
-template <typename K, int kDtype, int kPer>
-__device__ __forceinline__ bool choose(const Rule& r, const Keys& in, const float (&l)[kPer], const float (&b)[kPer],
-                                       int2* picked, int& mine) {
+// o: the ordered keys of this lane's experts (0: not there)
+template <typename K, bool kRaw, int kPer>
+__device__ __forceinline__ void keys_of(const Rule& r, const Keys& in, const float (&l)[kPer], const float (&b)[kPer],
+                                        typename Order<K>::O (&o)[kPer]) {
   using O = typename Order<K>::O;
-  constexpr bool kCheck = sizeof(K) == 4;
+  if (kRaw) {
+    // from the key of -inf, which becomes 0, to those of finite scores
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) o[i] = ordered((K)l[i]) - ordered((K)-INFINITY);
+    return;
+  }
+  const K top = (K)in.top;
+  K scale = (K)in.scale;
+  if (sizeof(K) == 8 && r.score == LAPSUM_SCORE_SOFTMAX) {
+    K s = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (l[i] != -INFINITY) s += exp_of((K)l[i] - top);
+    scale = quotient((K)1, warp_sum(s));
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    K s = (K)l[i];
+    if (r.score == LAPSUM_SCORE_SOFTMAX) s = exp_of(s - top) * scale;
+    if (r.score == LAPSUM_SCORE_SIGMOID) s = quotient((K)1, (K)1 + exp_of(-s));
+    o[i] = l[i] == -INFINITY ? O(0) : ordered(s + (K)b[i]);
+  }
+}
+
+// Clears the keys of the groups that go.  Returns whether the lowest value that
+// stays and the highest that goes are apart by more than fp32's error (kCheck).
+template <typename K, bool kCheck, int kPer>
+__device__ __forceinline__ bool keep_groups(const Rule& r, const Keys& in, const float (&l)[kPer],
+                                            typename Order<K>::O (&o)[kPer]) {
+  using O = typename Order<K>::O;
   const int lane = threadIdx.x & 31;
-  O o[kPer];
-  bool certain = true;
-  if (r.raw) {
+  // the value of group g: in all its lanes, or in lane g where they are not whole
+  O first = 0, second = 0;
+  int g = lane, lanes = 1;
+  if (r.lanes) {
+    lanes = r.lanes;
+    g = lane / lanes;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = l[i] == -INFINITY ? O(0) : ordered((K)l[i]);
+    for (int i = 0; i < kPer; ++i) top_two(first, second, o[i], O(0));
+    for (int d = 1; d < lanes; d <<= 1) {
+      const O c = shuffle_xor(first, d), e = shuffle_xor(second, d);
+      top_two(first, second, c, e);
+    }
   } else {
-    K top = 0, scale = 1;
-    if (r.score == LAPSUM_SCORE_SOFTMAX) {
-      float m = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) m = fmaxf(m, l[i]);
-      top = (K)warp_max(m);
-      K s = 0;
+    for (int q = 0; q < r.groups; ++q) {
+      const int e0 = q * r.size - lane * kPer, e1 = e0 + r.size;
+      O c = 0, e = 0;
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (l[i] != -INFINITY) s += exp_of((K)l[i] - top);
-      scale = quotient((K)1, warp_sum(s));
+        if (i >= e0 && i < e1) top_two(c, e, o[i], O(0));
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const O x = shuffle_xor(c, d), y = shuffle_xor(e, d);
+        top_two(c, e, x, y);
+      }
+      if (lane == q) {
+        first = c;
+        second = e;
+      }
     }
+  }
+  const O from = r.raw ? ordered((K)-INFINITY) : O(0);
+  K value = first ? key_of(first + from) : (K)-INFINITY;
+  if (r.top == 2 && second) value += key_of(second + from);
+  if (g >= r.groups) value = -INFINITY;
+  int above = 0;
+  for (int q = 0; q < r.groups; ++q) {
+    const K v = __shfl_sync(kAll, value, q * lanes);
+    above += (v > value || (v == value && q < g)) ? 1 : 0;
+  }
+  const bool stays = g < r.groups && above < r.kept;
+  bool certain = true;
+  if (kCheck && !r.raw) {
+    // a value is the sum of up to two keys, each within 2^-18 of its score and
+    // 2^-24 of itself, and scores are at most a key plus the largest bias
+    const float lo = -warp_max(stays ? -(float)value : -INFINITY);
+    const float hi = warp_max(stays || g >= r.groups ? -INFINITY : (float)value);
+    float size = fabsf(lo) + fabsf(hi) + 4.0f * in.bias_max, unit = 7.7e-6f;
+    if (r.score == LAPSUM_SCORE_IDENTITY) {
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (l[i] != -INFINITY) m = fmaxf(m, fabsf(l[i]));
+      size = 4.0f * (warp_max(m) + in.bias_max);
+      unit = 2.4e-7f;
+    }
+    certain = hi == -INFINITY || lo - hi > unit * size + 1e-37f;
+  }
+  if (r.lanes) {
+    if (!stays) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) o[i] = 0;
+    }
+  } else {
+    const uint32_t stay = __ballot_sync(kAll, stays);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      K s = (K)l[i];
-      if (r.score == LAPSUM_SCORE_SOFTMAX) s = exp_of(s - top) * scale;
-      if (r.score == LAPSUM_SCORE_SIGMOID) s = quotient((K)1, (K)1 + exp_of(-s));
-      o[i] = l[i] == -INFINITY ? O(0) : ordered(s + (K)b[i]);
+      const int e = lane * kPer + i;
+      if (e < r.experts && !(stay >> (e / r.size) & 1u)) o[i] = 0;
     }
   }
-  if (r.kept < r.groups) {
-    // the value of group g: in all its lanes, or in lane g where they are not whole
-    O first = 0, second = 0;
-    int g = lane, lanes = 1;
-    if (r.lanes) {
-      lanes = r.lanes;
-      g = lane / lanes;
+  return certain;
+}
+
+// o in descending order (Batcher's odd-even merge sort)
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&o)[N]) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) top_two(first, second, o[i], O(0));
-      for (int d = 1; d < lanes; d <<= 1) {
-        const O c = shuffle_xor(first, d), e = shuffle_xor(second, d);
-        top_two(first, second, c, e);
-      }
-    } else {
-      for (int q = 0; q < r.groups; ++q) {
-        const int e0 = q * r.size - lane * kPer, e1 = e0 + r.size;
-        O c = 0, e = 0;
+  for (int p = 1; p < N; p *= 2)
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (i >= e0 && i < e1) top_two(c, e, o[i], O(0));
+    for (int q = p; q >= 1; q /= 2)
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const O x = shuffle_xor(c, d), y = shuffle_xor(e, d);
-          top_two(c, e, x, y);
-        }
-        if (lane == q) {
-          first = c;
-          second = e;
-        }
-      }
-    }
-    K value = first ? key_of(first) : (K)-INFINITY;
-    if (r.top == 2 && second) value += key_of(second);
-    if (g >= r.groups) value = -INFINITY;
-    int above = 0;
-    for (int q = 0; q < r.groups; ++q) {
-      const K v = __shfl_sync(kAll, value, q * lanes);
-      above += (v > value || (v == value && q < g)) ? 1 : 0;
-    }
-    const bool stays = g < r.groups && above < r.kept;
-    if (kCheck && !r.raw) {
-      // the lowest value that stays against the highest that goes; a value is
-      // the sum of up to two keys, each within 2^-18 of its score and 2^-24 of
-      // itself, and scores are at most a key plus the largest bias
-      const float lo = -warp_max(stays ? -(float)value : -INFINITY);
-      const float hi = warp_max(stays || g >= r.groups ? -INFINITY : (float)value);
-      float size = fabsf(lo) + fabsf(hi) + 4.0f * in.bias_max, unit = 7.7e-6f;
-      if (r.score == LAPSUM_SCORE_IDENTITY) {
-        float m = 0.0f;
+      for (int j = q % p; j + q < N; j += 2 * q)
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (l[i] != -INFINITY) m = fmaxf(m, fabsf(l[i]));
-        size = 4.0f * (warp_max(m) + in.bias_max);
-        unit = 2.4e-7f;
-      }
-      certain = hi == -INFINITY || lo - hi > unit * size + 1e-37f;
-    }
-    if (r.lanes) {
-      if (!stays) {
+        for (int i = 0; i < q; ++i)
+          if (j + i + q < N && (j + i) / (2 * p) == (j + i + q) / (2 * p)) {
+            const uint32_t a = o[j + i], b = o[j + i + q];
+            o[j + i] = max(a, b);
+            o[j + i + q] = min(a, b);
+          }
+}
+
+// Lane j < k gets the token's j-th choice (or -1) in `mine`.  l: this lane's
+// scores, -inf where masked; b: its biases; picked: k + 1 places in shared
+// memory.  False where fp32 keys cannot tell.
+template <int kDtype, int kPer, bool kRaw>
+__device__ __forceinline__ bool choose(const Rule& r, const Keys& in, const float (&l)[kPer], const float (&b)[kPer],
+                                       int* picked, int& mine) {
+  const int lane = threadIdx.x & 31;
+  uint32_t o[kPer];
+  keys_of<float, kRaw>(r, in, l, b, o);
+  bool certain = true;
+  if (r.kept < r.groups) certain = keep_groups<float, !kRaw>(r, in, l, o);
+  // exact: the bits that make room for the place in the lane were 0 anyway
+  bool exact = kRaw;
+  if (kRaw && kDtype == LAPSUM_F32) {
+    uint32_t low = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) o[i] = 0;
-      }
-    } else {
-      const uint32_t stay = __ballot_sync(kAll, stays);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int e = lane * kPer + i;
-        if (e < r.experts && !(stay >> (e / r.size) & 1u)) o[i] = 0;
-      }
-    }
+    for (int i = 0; i < kPer; ++i) low |= __float_as_uint(l[i]);
+    exact = !__any_sync(kAll, (low & 31u) != 0u);
   }
-  const int rounds = kCheck && !r.raw ? r.k + 1 : r.k;  // with the choice that would follow
-  if (lane < rounds || lane == 0) picked[lane] = make_int2(-1, 0);
-  if (lane == 0) picked[r.k] = make_int2(-1, 0);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) o[i] = (o[i] & ~31u) | (31u - i);  // below 32: nothing there
+  sort_down(o);
+  const int rounds = exact ? r.k : r.k + 1;  // with the choice that would follow
+  for (int j = lane; j <= r.k; j += 32) picked[j] = -1;
   __syncwarp();
   for (int j = 0; j < rounds; ++j) {
-    O best = o[0];
+    const uint32_t head = o[0] & ~31u, m = __reduce_max_sync(kAll, head);
+    if (m == 0) break;  // nothing left
+    // equal keys: the lowest lane, in it the lowest place
+    const bool win = lane == __ffs(__ballot_sync(kAll, head == m)) - 1;
+    if (win) picked[j] = lane * kPer + 31 - (int)(o[0] & 31u);
+#pragma unroll
+    for (int i = 0; i + 1 < kPer; ++i) o[i] = win ? o[i + 1] : o[i];
+    o[kPer - 1] = win ? 0u : o[kPer - 1];
+  }
+  __syncwarp();
+  mine = lane < r.k ? picked[lane] : -1;
+  if (!exact) {
+    // neighbours in the order: apart by more than their errors, or truly equal;
+    // the last place also by more than the bits that were replaced (2^-18)
+    const int e1 = mine >= 0 ? picked[lane + 1] : -1;
+    if (e1 >= 0) {
+      const float score = load_score<kDtype>(in.scores, in.at + mine), score1 = load_score<kDtype>(in.scores, in.at + e1);
+      float key = score, key1 = score1, bound = 0.0f;
+      bool same = score == score1;
+      if (!kRaw) {
+        const float bias = in.bias ? __ldg(in.bias + mine) : 0.0f, bias1 = in.bias ? __ldg(in.bias + e1) : 0.0f;
+        same = same && bias == bias1;
+        if (r.score == LAPSUM_SCORE_IDENTITY) {
+          key = score + bias;
+          key1 = score1 + bias1;
+        } else {
+          float s, s1;
+          if (r.score == LAPSUM_SCORE_SIGMOID) {
+            s = quotient(1.0f, 1.0f + exp_of(-score));
+            s1 = quotient(1.0f, 1.0f + exp_of(-score1));
+          } else {
+            s = exp_of(score - in.top) * in.scale;
+            s1 = exp_of(score1 - in.top) * in.scale;
+          }
+          key = s + bias;
+          key1 = s1 + bias1;
+          bound = 7.7e-6f * (s + s1);
+        }
+        bound += 2.4e-7f * (fabsf(key) + fabsf(key1)) + 1e-37f;  // the last: flushed subnormals
+      }
+      if (lane == r.k - 1) {
+        bound += 4e-6f * fabsf(key1) + 1e-37f;
+        same = false;
+      }
+      if (!(key - key1 > bound) && !same) certain = false;
+    }
+    certain = __all_sync(kAll, certain);
+  }
+  __syncwarp();
+  return certain;
+}
+
+// The same with fp64 keys, none of whose bits is replaced.
+template <int kPer>
+__device__ __forceinline__ int choose_exact(const Rule& r, const Keys& in, const float (&l)[kPer], const float (&b)[kPer],
+                                            int* picked) {
+  const int lane = threadIdx.x & 31;
+  uint64_t o[kPer];
+  if (r.raw)
+    keys_of<double, true>(r, in, l, b, o);
+  else
+    keys_of<double, false>(r, in, l, b, o);
+  if (r.kept < r.groups) keep_groups<double, false>(r, in, l, o);
+  for (int j = lane; j < r.k; j += 32) picked[j] = -1;
+  __syncwarp();
+  for (int j = 0; j < r.k; ++j) {
+    uint64_t best = o[0];
 #pragma unroll
     for (int i = 1; i < kPer; ++i) best = max(best, o[i]);
-    const O m = warp_top(best);
-    if (m == 0) break;  // nothing left
+    const uint64_t m = warp_top(best);
+    if (m == 0) break;
     if (lane == __ffs(__ballot_sync(kAll, best == m)) - 1) {
       int at = 0;
 #pragma unroll
@@ -246,28 +356,13 @@ __device__ __forceinline__ bool choose(const Rule& r, const Keys& in, const floa
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
         if (i == at) o[i] = 0;
-      picked[j] = make_int2(lane * kPer + at, __float_as_int((float)key_of(m)));
+      picked[j] = lane * kPer + at;
     }
   }
   __syncwarp();
-  mine = lane < r.k ? picked[lane].x : -1;
-  if (kCheck && !r.raw) {
-    // neighbours in the order: apart by more than both errors, or truly equal
-    if (mine >= 0) {
-      const int e1 = picked[lane + 1].x;
-      if (e1 >= 0) {
-        const float key = __int_as_float(picked[lane].y), key1 = __int_as_float(picked[lane + 1].y);
-        const float score = load_score<kDtype>(in.scores, in.at + mine), score1 = load_score<kDtype>(in.scores, in.at + e1);
-        const float bias = in.bias ? __ldg(in.bias + mine) : 0.0f, bias1 = in.bias ? __ldg(in.bias + e1) : 0.0f;
-        float bound = 2.4e-7f * (fabsf(key) + fabsf(key1)) + 1e-37f;  // the last: flushed subnormals
-        if (r.score != LAPSUM_SCORE_IDENTITY) bound += 7.7e-6f * (fabsf(key - bias) + fabsf(key1 - bias1));
-        if (!(score == score1 && bias == bias1) && !(key - key1 > bound)) certain = false;
-      }
-    }
-    certain = __all_sync(kAll, certain);
-  }
+  const int mine = lane < r.k ? picked[lane] : -1;
   __syncwarp();
-  return certain;
+  return mine;
 }
 
 // kPer neighbouring scores; vec: as one access of up to 16 bytes each
@@ -339,40 +434,65 @@ __device__ __forceinline__ void store_scores(void* grad, int64_t at, int n, bool
   }
 }
 
-// This lane's scores and biases, -inf where masked (padding included).  False
-// when the token holds a NaN or +inf that is not masked.
-template <int kDtype, int kPer>
-__device__ __forceinline__ bool load_token(const void* scores, int64_t at, const float* bias, int experts, bool vec,
-                                           float (&l)[kPer], float (&b)[kPer]) {
-  const int lane = threadIdx.x & 31, e0 = lane * kPer, n = max(0, min(kPer, experts - e0));
-  load_scores<kDtype, kPer>(scores, at + e0, n, vec, l);
+// This lane's biases (0 without); vec: E is whole lanes and they lie on 16 bytes.
+template <int kPer>
+__device__ __forceinline__ void load_biases(const float* bias, int experts, bool vec, float (&b)[kPer]) {
+  const int e0 = (threadIdx.x & 31) * kPer, n = max(0, min(kPer, experts - e0));
+  if (bias && n > 0) {
+    load_scores<LAPSUM_F32, kPer>(bias, e0, n, vec, b);
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (!bias || i >= n) b[i] = 0.0f;
+}
+
+// l: -inf where a score or bias masks.  False when the token holds a NaN or
+// +inf that is not masked.
+template <bool kBias, int kPer>
+__device__ __forceinline__ bool mask_token(float (&l)[kPer], const float (&b)[kPer]) {
   bool fine = true;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    b[i] = bias && i < n ? __ldg(bias + e0 + i) : 0.0f;
-    if (b[i] == -INFINITY) l[i] = -INFINITY;
-    if (l[i] != -INFINITY && !(l[i] < INFINITY && b[i] < INFINITY)) fine = false;
+    if (kBias && b[i] == -INFINITY) l[i] = -INFINITY;
+    if (!(l[i] < INFINITY && (!kBias || l[i] == -INFINITY || b[i] < INFINITY))) fine = false;
   }
   return __all_sync(kAll, fine);
 }
 
-// The choice in fp64, for a token whose fp32 keys lie too close.
+// This lane's scores of the token, padding -inf
 template <int kDtype, int kPer>
-__device__ __noinline__ int choose_again(const Rule& r, const Keys& in, int2* picked) {
+__device__ __forceinline__ void load_token(const void* scores, int64_t at, int experts, bool vec, float (&l)[kPer]) {
+  const int e0 = (threadIdx.x & 31) * kPer;
+  load_scores<kDtype, kPer>(scores, at + e0, max(0, min(kPer, experts - e0)), vec, l);
+}
+
+// The choice of a token whose fp32 keys lie too close.
+template <int kDtype, int kPer>
+__device__ __noinline__ int choose_again(Rule r, Keys in, int* picked) {
   float l[kPer], b[kPer];
-  load_token<kDtype, kPer>(in.scores, in.at, in.bias, r.experts, false, l, b);
-  int mine;
-  choose<double, kDtype, kPer>(r, in, l, b, picked, mine);
-  return mine;
+  load_token<kDtype, kPer>(in.scores, in.at, r.experts, false, l);
+  load_biases<kPer>(in.bias, r.experts, false, b);
+  mask_token<true>(l, b);
+  return choose_exact<kPer>(r, in, l, b, picked);
+}
+
+// sums and maxima over the k lanes that hold a choice (the others: neutral)
+__device__ __forceinline__ float chosen_max(float v, int k) {
+  for (int d = 1; d < k; d <<= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+  return v;
+}
+__device__ __forceinline__ float chosen_sum(float v, int k) {
+  for (int d = 1; d < k; d <<= 1) v += __shfl_xor_sync(kAll, v, d);
+  return v;
 }
 
 // log of the sigmoid, without overflow
 __device__ __forceinline__ float log_sigmoid(float l) { return fminf(l, 0.0f) - log1pf(expf(-fabsf(l))); }
 
-template <int kDtype, int kPer>
-__global__ void __launch_bounds__(kThreads) k_route_fwd(const RouteFwd a) {
-  __shared__ int2 all_picked[kWarps][LAPSUM_EXPERTS_MAX_K + 1];
-  int2* picked = all_picked[threadIdx.x >> 5];
+template <int kDtype, int kPer, bool kRaw>
+__global__ void __launch_bounds__(kThreads, kPer <= 8 ? 8 : kPer == 16 ? 6 : 3) k_route_fwd(const RouteFwd a) {
+  __shared__ int all_picked[kWarps][LAPSUM_EXPERTS_MAX_K + 1];
+  int* picked = all_picked[threadIdx.x >> 5];
   const int lane = threadIdx.x & 31;
   Rule r;
   r.experts = a.experts;
@@ -382,15 +502,24 @@ __global__ void __launch_bounds__(kThreads) k_route_fwd(const RouteFwd a) {
   r.size = a.experts / a.groups;
   r.kept = a.groups_kept;
   r.top = a.group_top;
-  r.raw = !a.bias && (a.groups_kept == a.groups || a.group_top == 1);
+  r.raw = kRaw;
   r.lanes = r.size % kPer == 0 && ((r.size / kPer) & (r.size / kPer - 1)) == 0 ? r.size / kPer : 0;
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.tokens; t += (int64_t)gridDim.x * kWarps) {
-    float l[kPer], b[kPer];
+  const bool soft = a.score == LAPSUM_SCORE_SOFTMAX && (!r.raw || !a.renormalize);
+  const int64_t step = (int64_t)gridDim.x * kWarps;
+  int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  float b[kPer], ahead[kPer];
+  if (!kRaw) load_biases<kPer>(a.bias, a.experts, a.bias_vec, b);
+  if (t < a.tokens) load_token<kDtype, kPer>(a.scores, t * a.stride, a.experts, a.vec, ahead);
+  for (; t < a.tokens; t += step) {
+    float l[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) l[i] = ahead[i];
+    if (t + step < a.tokens) load_token<kDtype, kPer>(a.scores, (t + step) * a.stride, a.experts, a.vec, ahead);
     Keys in;
     in.scores = a.scores;
     in.at = t * a.stride;
     in.bias = a.bias;
-    const bool fine = load_token<kDtype, kPer>(a.scores, in.at, a.bias, a.experts, a.vec, l, b);
+    const bool fine = mask_token<!kRaw>(l, b);
     int mine = -1;
     float w = 0.0f;
     if (fine) {
@@ -402,30 +531,32 @@ __global__ void __launch_bounds__(kThreads) k_route_fwd(const RouteFwd a) {
         m = warp_max(m);
       }
       in.bias_max = m;
-      if (!choose<float, kDtype, kPer>(r, in, l, b, picked, mine)) mine = choose_again<kDtype, kPer>(r, in, picked);
+      if (soft) {
+        float top = -INFINITY, total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) top = fmaxf(top, l[i]);
+        in.top = warp_max(top);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (l[i] != -INFINITY) total += __expf(l[i] - in.top);
+        in.scale = 1.0f / warp_sum(total);
+      }
+      if (!choose<kDtype, kPer, kRaw>(r, in, l, b, picked, mine)) mine = choose_again<kDtype, kPer>(r, in, picked);
       const float s = mine >= 0 ? load_score<kDtype>(a.scores, in.at + mine) : -INFINITY;
       if (a.renormalize) {
         if (a.score == LAPSUM_SCORE_IDENTITY) {
           const float v = mine >= 0 ? s : 0.0f;
-          const float total = warp_sum(v);
-          w = total != 0.0f ? a.scale * v / total : 0.0f;
+          const float total = chosen_sum(v, a.k);
+          w = total != 0.0f ? a.scale * (v / total) : 0.0f;
         } else {  // softmax over the chosen of log s: no sum can vanish
           const float v = a.score == LAPSUM_SCORE_SIGMOID && mine >= 0 ? log_sigmoid(s) : s;
-          const float top = warp_max(v);
+          const float top = chosen_max(v, a.k);
           const float p = mine >= 0 ? expf(v - top) : 0.0f;
-          const float total = warp_sum(p);
-          w = mine >= 0 ? a.scale * p / total : 0.0f;
+          const float total = chosen_sum(p, a.k);
+          w = mine >= 0 ? a.scale * __fdividef(p, total) : 0.0f;  // 1 <= total <= k
         }
       } else if (a.score == LAPSUM_SCORE_SOFTMAX) {
-        float top = -INFINITY, total = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) top = fmaxf(top, l[i]);
-        top = warp_max(top);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (l[i] != -INFINITY) total += __expf(l[i] - top);
-        total = warp_sum(total);
-        w = mine >= 0 ? a.scale * expf(s - top) / total : 0.0f;
+        w = mine >= 0 ? a.scale * (expf(s - in.top) * in.scale) : 0.0f;
       } else if (mine >= 0) {
         w = a.scale * (a.score == LAPSUM_SCORE_SIGMOID ? 1.0f / (1.0f + expf(-s)) : s);
       }
@@ -489,7 +620,9 @@ __global__ void __launch_bounds__(kThreads) k_route_bwd(const RouteBwd a) {
     for (int i = 0; i < kPer; ++i) v[i] = bad ? __int_as_float(0x7fc00000) : 0.0f;
     if (dense && !bad) {
       float b[kPer], top = -INFINITY, total = 0.0f;
-      load_token<kDtype, kPer>(a.scores, at, a.bias, a.experts, a.vec, v, b);
+      load_token<kDtype, kPer>(a.scores, at, a.experts, a.vec, v);
+      load_biases<kPer>(a.bias, a.experts, a.bias_vec, b);
+      mask_token<true>(v, b);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) top = fmaxf(top, v[i]);
       top = warp_max(top);
@@ -512,7 +645,10 @@ __global__ void __launch_bounds__(kThreads) k_route_bwd(const RouteBwd a) {
 
 template <int kDtype, int kPer>
 void fwd_as(const RouteFwd& a, unsigned grid, cudaStream_t st) {
-  k_route_fwd<kDtype, kPer><<<grid, kThreads, 0, st>>>(a);
+  if (!a.bias && (a.groups_kept == a.groups || a.group_top == 1))
+    k_route_fwd<kDtype, kPer, true><<<grid, kThreads, 0, st>>>(a);
+  else
+    k_route_fwd<kDtype, kPer, false><<<grid, kThreads, 0, st>>>(a);
 }
 template <int kDtype, int kPer>
 void bwd_as(const RouteBwd& a, unsigned grid, cudaStream_t st) {
@@ -543,24 +679,27 @@ bool whole_lanes(const void* p, int64_t stride, int dtype, int experts) {
   return experts % per == 0 && (uintptr_t)p % bytes == 0 && stride * size % bytes == 0;
 }
 
-unsigned blocks_for(int64_t tokens) {
-  return (unsigned)std::min<int64_t>((tokens + kWarps - 1) / kWarps, 1 << 20);
+// resident blocks, each walking tokens with the next one's scores on their way
+unsigned blocks_for(int64_t tokens, int sms) {
+  return (unsigned)std::min<int64_t>((tokens + kWarps - 1) / kWarps, (int64_t)sms * 8);
 }
 
 }  // namespace
 
-cudaError_t launch_route_fwd(RouteFwd a, cudaStream_t st) {
+cudaError_t launch_route_fwd(RouteFwd a, int sms, cudaStream_t st) {
   a.vec = whole_lanes(a.scores, a.stride, a.dtype, a.experts);
-  const unsigned grid = blocks_for(a.tokens);
+  a.bias_vec = whole_lanes(a.bias, 0, LAPSUM_F32, a.experts);
+  const unsigned grid = blocks_for(a.tokens, sms);
   Launch guard("k_route_fwd", st);
   LAPSUM_BY_TYPE(fwd_as, a, grid, st);
   return cudaGetLastError();
 }
 
-cudaError_t launch_route_bwd(RouteBwd a, cudaStream_t st) {
+cudaError_t launch_route_bwd(RouteBwd a, int sms, cudaStream_t st) {
   a.vec = whole_lanes(a.scores, a.stride, a.dtype, a.experts);
+  a.bias_vec = whole_lanes(a.bias, 0, LAPSUM_F32, a.experts);
   a.grad_vec = whole_lanes(a.grad, a.grad_stride, a.dtype, a.experts);
-  const unsigned grid = blocks_for(a.tokens);
+  const unsigned grid = blocks_for(a.tokens, sms);
   Launch guard("k_route_bwd", st);
   LAPSUM_BY_TYPE(bwd_as, a, grid, st);
   return cudaGetLastError();
