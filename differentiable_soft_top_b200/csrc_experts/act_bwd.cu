@@ -10,6 +10,7 @@
 #include <cuda_fp16.h>
 
 #include "activation.cuh"
+#include "chain.cuh"
 #include "experts.h"
 
 namespace lapsum {
@@ -97,6 +98,8 @@ __device__ __forceinline__ void fill_table(const int32_t* offsets, int64_t rows,
 
 template <bool kGated>
 __global__ void __launch_bounds__(kThreads) k_act_bwd(const ActArgs a, int max_tiles) {
+  grid_launch_next();
+  grid_wait_previous();
   __shared__ int table[kMaxTable + 1];
   __shared__ float red[2][8][kCols];
   const int col = threadIdx.x & 31, lane8 = threadIdx.x >> 5;
@@ -188,6 +191,8 @@ __global__ void __launch_bounds__(kThreads) k_act_bwd(const ActArgs a, int max_t
 // 8 lanes take every 8th tile each, then join in the order of the lanes.
 __global__ void __launch_bounds__(kThreads) k_bias_sum(const float* part, int out, int64_t rows, int experts,
                                                        const int32_t* offsets, int max_tiles, int bf16, uint16_t* gb) {
+  grid_launch_next();
+  grid_wait_previous();
   __shared__ float red[8][32];
   __shared__ int table[kMaxTable + 1];
   const int e = blockIdx.y, c = blockIdx.x * 32 + (threadIdx.x & 31), l = threadIdx.x >> 5;
@@ -238,14 +243,14 @@ cudaError_t launch_act_bwd(const void* grad_y, int bf16, int64_t rows, int64_t o
   {
     Launch guard("k_act_bwd", st);
     if (gated)
-      k_act_bwd<true><<<(unsigned)grid, kThreads, 0, st>>>(a, (int)bound);
+      launch_ex(true, k_act_bwd<true>, dim3((unsigned)grid), dim3(kThreads), 0, st, a, (int)bound);
     else
-      k_act_bwd<false><<<(unsigned)grid, kThreads, 0, st>>>(a, (int)bound);
+      launch_ex(true, k_act_bwd<false>, dim3((unsigned)grid), dim3(kThreads), 0, st, a, (int)bound);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !grad_bias) return e;
   Launch guard("k_bias_sum", st);
-  k_bias_sum<<<dim3((unsigned)((out + 31) / 32), (unsigned)experts), kThreads, 0, st>>>(
+  launch_ex(true, k_bias_sum, dim3((unsigned)((out + 31) / 32), (unsigned)experts), dim3(kThreads), 0, st,
       a.part, a.out, rows, experts, offsets, (int)bound, bf16, static_cast<uint16_t*>(grad_bias));
   return cudaGetLastError();
 }

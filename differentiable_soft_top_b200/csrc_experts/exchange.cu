@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "chain.cuh"
 #include "experts.h"
 
 namespace lapsum {
@@ -39,8 +40,10 @@ PlanShape plan_shape(int64_t slots) {
 
 __global__ void __launch_bounds__(kPlanThreads) k_plan_count(const int32_t* chosen, int64_t slots, int experts, int per,
                                                              int32_t* hist) {
+  grid_launch_next();
   __shared__ int cnt[LAPSUM_EXPERTS_MAX];
   for (int e = threadIdx.x; e < experts; e += kPlanThreads) cnt[e] = 0;
+  grid_wait_previous();
   __syncthreads();
   const int64_t s0 = (int64_t)blockIdx.x * per, s1 = min(slots, s0 + per);
   for (int64_t s = s0 + threadIdx.x; s < s1; s += kPlanThreads) {
@@ -55,6 +58,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_count(const int32_t* chos
 __global__ void __launch_bounds__(kPlanThreads) k_plan_place(const int32_t* chosen, int64_t slots, int experts, int per,
                                                              const int32_t* hist, int32_t* offsets, int32_t* rows,
                                                              int32_t* slot_of) {
+  grid_launch_next();
   extern __shared__ int sh[];
   int* total = sh;                       // [experts]
   int* start = sh + experts;             // [experts] first row of this block's slots of an expert
@@ -63,6 +67,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_place(const int32_t* chos
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t s0 = (int64_t)blockIdx.x * per, s1 = min(slots, s0 + per);
   for (int i = threadIdx.x; i < kPlanWarps * experts; i += kPlanThreads) mine[i] = 0;
+  grid_wait_previous();
   __syncthreads();
   const int64_t part = per / kPlanWarps;  // a multiple of 32
   const int64_t w0 = s0 + warp * part, w1 = min(s1, w0 + part);
@@ -195,6 +200,8 @@ __global__ void __launch_bounds__(kRowThreads) k_dispatch(const typename Elem<kD
                                                           typename Elem<kDtype>::T* __restrict__ out, int64_t out_stride,
                                                           int64_t slots, Units u) {
   using P = Pack<kDtype, kVec>;
+  grid_launch_next();
+  grid_wait_previous();
   const int lane = threadIdx.x & 31;
   const int64_t nwarp = (int64_t)gridDim.x * (kRowThreads / 32);
   for (int64_t w = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); w < u.rows * u.parts; w += nwarp) {
@@ -227,6 +234,8 @@ __global__ void __launch_bounds__(kRowThreads)
               const typename Elem<kDtype>::T* __restrict__ residual, int64_t res_stride,
               typename Elem<kDtype>::T* __restrict__ out, int64_t out_stride, int packs, int per_row) {
   using P = Pack<kDtype, kVec>;
+  grid_launch_next();
+  grid_wait_previous();
   const int in_block = kRowThreads / per_row;
   const int64_t step = (int64_t)gridDim.x * in_block;
   int64_t t = (int64_t)blockIdx.x * in_block + threadIdx.x / per_row;
@@ -300,6 +309,8 @@ __global__ void __launch_bounds__(kRowThreads)
                   const int32_t* __restrict__ rows, const int32_t* __restrict__ slot_of, int k, int64_t slots,
                   typename Elem<kDtype>::T* __restrict__ gy, int64_t gy_stride, float* __restrict__ gw, int packs) {
   using P = Pack<kDtype, kVec>;
+  grid_launch_next();
+  grid_wait_previous();
   const int lane = threadIdx.x & 31;
   const int64_t nwarp = (int64_t)gridDim.x * (kRowThreads / 32);
   for (int64_t s = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); s < slots; s += nwarp) {
@@ -370,7 +381,7 @@ void dispatch_as(const void* x, int64_t tokens, int k, int64_t dim, int64_t x_st
                  int64_t out_stride, int sms, cudaStream_t st) {
   using T = typename Elem<kDtype>::T;
   const Units u = make_units(tokens * k, dim / kVec, sms);
-  k_dispatch<kDtype, kVec><<<grid_of(u.rows * u.parts, sms), kRowThreads, 0, st>>>(
+  launch_ex(true, k_dispatch<kDtype, kVec>, dim3(grid_of(u.rows * u.parts, sms)), dim3(kRowThreads), 0, st,
       static_cast<const T*>(x), x_stride, slot_of, k, static_cast<T*>(out), out_stride, tokens * k, u);
 }
 template <int kDtype, int kVec>
@@ -383,7 +394,7 @@ void combine_as(const void* y, int64_t tokens, int k, int64_t dim, int64_t y_str
   while (per_row < kRowThreads && per_row * each < packs) per_row *= 2;
   const int64_t blocks = (tokens + kRowThreads / per_row - 1) / (kRowThreads / per_row);
   auto* kernel = k <= 2 ? k_combine<kDtype, kVec, 2, 4> : k <= 4 ? k_combine<kDtype, kVec, 4, 2> : k_combine<kDtype, kVec, 8, 1>;
-  kernel<<<(unsigned)std::min<int64_t>(blocks, (int64_t)sms * 8), kRowThreads, 0, st>>>(
+  launch_ex(true, kernel, dim3((unsigned)std::min<int64_t>(blocks, (int64_t)sms * 8)), dim3(kRowThreads), 0, st,
       static_cast<const T*>(y), y_stride, weights, rows, tokens, k, tokens * k, static_cast<const T*>(residual), res_stride,
       static_cast<T*>(out), out_stride, packs, per_row);
 }
@@ -392,7 +403,7 @@ void combine_bwd_as(const void* grad, int64_t tokens, int k, int64_t dim, int64_
                     int64_t y_stride, const float* weights, const int32_t* rows, const int32_t* slot_of, void* grad_y,
                     int64_t grad_y_stride, float* grad_weights, int sms, cudaStream_t st) {
   using T = typename Elem<kDtype>::T;
-  k_combine_bwd<kDtype, kVec><<<grid_of(tokens * k, sms), kRowThreads, 0, st>>>(
+  launch_ex(true, k_combine_bwd<kDtype, kVec>, dim3(grid_of(tokens * k, sms)), dim3(kRowThreads), 0, st,
       static_cast<const T*>(grad), grad_stride, static_cast<const T*>(y), y_stride, weights, rows, slot_of, k,
       tokens * k, static_cast<T*>(grad_y), grad_y_stride, grad_weights, (int)(dim / kVec));
 }
@@ -410,13 +421,13 @@ cudaError_t launch_plan(const int32_t* chosen, int64_t slots, int experts, int32
   int32_t* hist = p.blocks > 1 ? static_cast<int32_t*>(ws) : nullptr;
   if (hist) {
     Launch guard("k_plan_count", st);
-    k_plan_count<<<p.blocks, kPlanThreads, 0, st>>>(chosen, slots, experts, p.per, hist);
+    launch_ex(true, k_plan_count, dim3(p.blocks), dim3(kPlanThreads), 0, st, chosen, slots, experts, p.per, hist);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   Launch guard("k_plan_place", st);
-  k_plan_place<<<p.blocks, kPlanThreads, (size_t)(2 + kPlanWarps) * experts * 4, st>>>(chosen, slots, experts, p.per,
-                                                                                     hist, offsets, rows, slot_of);
+  launch_ex(true, k_plan_place, dim3(p.blocks), dim3(kPlanThreads), (size_t)(2 + kPlanWarps) * experts * 4, st, chosen, slots,
+            experts, p.per, (const int32_t*)hist, offsets, rows, slot_of);
   return cudaGetLastError();
 }
 

@@ -13,8 +13,8 @@
 //                    contraction runs over an expert's rows and its ragged
 //                    end is zeroed in shared memory
 //
-// One block of six warps: warp 0 fills a ring of stages by tiled copies (64
-// deep, 128-byte swizzle), warp 1 issues the products, warps 2-5 read the
+// In a block warp 0 fills a ring of stages by tiled copies (64 deep, 128-byte
+// swizzle), warp 1 issues the products, the other four or eight read the
 // accumulators from tensor memory and write the result.  Two accumulators let
 // the epilogue of one tile run beside the products of the next; blocks walk
 // the tiles with a stride of the grid.  Three forms, by the rows of an expert:
@@ -43,6 +43,7 @@
 #include <cuda_fp16.h>
 
 #include "activation.cuh"
+#include "chain.cuh"
 #include "experts.h"
 #include "umma.cuh"
 
@@ -51,7 +52,6 @@ namespace {
 
 enum Mode { kForward, kGradX, kGradW };
 
-constexpr int kThreads = 192;
 constexpr int kDepth = 64;              // contraction per stage: one 128-byte line
 constexpr int kLanes = 128;             // accumulator lanes of a block
 constexpr int kTokBox = 32;             // tokens per copied box of a ragged tile (a full one: one box)
@@ -79,6 +79,8 @@ template <int kMode, int kTok, bool kGated>
 struct Shape {
   static constexpr bool kPair = kTok == 256;
   static constexpr bool kSplit = kTok == 32;       // few rows: clusters, two blocks per SM
+  static constexpr int kEpilogue = kSplit ? 4 : 8;  // warps: one or two per quarter of the lanes
+  static constexpr int kThreads = 64 + 32 * kEpilogue;
   static constexpr int kFeat = kLanes / (kGated ? 2 : 1);           // features of a block's tile
   static constexpr int kTileFeat = kFeat * (kPair ? 2 : 1);         // of a tile
   static constexpr int kABytes = kLanes * 128;
@@ -87,7 +89,7 @@ struct Shape {
   static constexpr int kBudget = kSplit ? 100 * 1024 : 196 * 1024;
   static constexpr int kStages = kBudget / kStage;
   static constexpr int kTmemCols = kSplit ? 32 : 2 * kTok;
-  static constexpr int kStaging = kSplit ? 0 : 4 * 32 * kPitch;  // the split form stages in the ring
+  static constexpr int kStaging = kSplit ? 0 : kEpilogue * 32 * kPitch;  // the split form stages in the ring
   static constexpr int kTable = kMode == kGradW ? 0 : (LAPSUM_EXPERTS_MAX + 2) * 4;
   static constexpr int kSmem = kStages * kStage + kStaging + kTable + 1024 /* alignment */ + 512 /* barriers */;
 };
@@ -144,25 +146,32 @@ __device__ __forceinline__ void row_range(const Args& a, int e, int& lo, int& n)
 }
 
 // Token tiles before each expert, in shared memory: table[e] for e = 0 ..
-// experts + 1 (one warp).
+// experts + 1.  The whole block; ends with the block in step.
 template <int kTok>
-__device__ __forceinline__ void build_table(const Args& a, int* table, int lane) {
-  int base = 0;
-  for (int e0 = 0; e0 <= a.experts; e0 += 32) {
-    const int e = e0 + lane;
-    int lo = 0, n = 0;
-    if (e <= a.experts) row_range(a, e, lo, n);
-    int v = (n + kTok - 1) / kTok;
-    const int own = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, v, d);
-      if (lane >= d) v += u;
-    }
-    if (e <= a.experts) table[e] = base + v - own;
-    base += __shfl_sync(0xffffffffu, v, 31);
+__device__ __forceinline__ void build_table(const Args& a, int* table) {
+  const int lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e <= a.experts; e += blockDim.x) {
+    int lo, n;
+    row_range(a, e, lo, n);
+    table[e] = (n + kTok - 1) / kTok;
   }
-  if (lane == 0) table[a.experts + 1] = base;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int base = 0;
+    for (int e0 = 0; e0 <= a.experts; e0 += 32) {
+      const int e = e0 + lane, own = e <= a.experts ? table[e] : 0;
+      int v = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += u;
+      }
+      if (e <= a.experts) table[e] = base + v - own;
+      base += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) table[a.experts + 1] = base;
+  }
+  __syncthreads();
 }
 
 template <int kMode, int kTok, bool kGated>
@@ -408,7 +417,7 @@ __device__ __forceinline__ void fill(float (&v)[2][16], float x) {
 // map_f: the weights (kGradW: dH); map_t: the tokens' rows in small boxes,
 // map_full: in boxes of a full tile
 template <typename T, int kMode, int kTok, bool kGated>
-__global__ void __launch_bounds__(kThreads, Shape<kMode, kTok, kGated>::kSplit ? 2 : 1)
+__global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kMode, kTok, kGated>::kSplit ? 2 : 1)
     k_product(const __grid_constant__ CUtensorMap map_f, const __grid_constant__ CUtensorMap map_t,
               const __grid_constant__ CUtensorMap map_full, const Args a, int tiles_grad_w) {
   using S = Shape<kMode, kTok, kGated>;
@@ -429,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kMode, kTok, kGated>::kSplit ?
   volatile uint32_t* gave_up = tmem_at + 1;
   int* table = reinterpret_cast<int*>(tail + 512);
 
+  grid_launch_next();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = kPair ? (int)cluster_rank() : 0;
   if (threadIdx.x == 0) {
@@ -441,13 +451,14 @@ __global__ void __launch_bounds__(kThreads, Shape<kMode, kTok, kGated>::kSplit ?
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full + b, 1);
-      mbar_init(acc_empty + b, kPair ? 8 : 4);
+      mbar_init(acc_empty + b, S::kEpilogue * (kPair ? 2 : 1));
     }
     mbar_init(drained, 1);
     *gave_up = 0u;
   }
   if (warp == 1) tmem_alloc<kPair>(tmem_at, S::kTmemCols);
-  if (kMode != kGradW && warp == 2) build_table<kTok>(a, table, lane);
+  grid_wait_previous();  // from here on the kernels before this one have finished
+  if (kMode != kGradW) build_table<kTok>(a, table);
   tc_fence_before();
   __syncthreads();
   if (kPair) cluster_sync();  // the other block's barriers are set up
@@ -620,8 +631,9 @@ __global__ void __launch_bounds__(kThreads, Shape<kMode, kTok, kGated>::kSplit ?
       }
     }
   } else if (!S::kSplit) {
-    const int quarter = warp & 3;  // the lanes of tensor memory this warp may read
-    const uint32_t base = smem_u32(staging) + quarter * 32 * kPitch;
+    // Two warps share a quarter of the lanes and take every other 32 columns.
+    const int quarter = warp & 3, part = (warp - 2) >> 2;
+    const uint32_t base = smem_u32(staging) + (warp - 2) * 32 * kPitch;
     uint32_t done = 0;
     bool ok = true;
     for (int tile = first; tile < tiles; tile += step) {
@@ -634,27 +646,30 @@ __global__ void __launch_bounds__(kThreads, Shape<kMode, kTok, kGated>::kSplit ?
       uint4 res[Frag<kGated>::kGroups];
       if (kMode == kForward) {
         load_bias<T, kGated>(a, t, feat0, bias, lane);
-        if (a.residual) get_rows<kGated>(res, a.residual, t.row0, a.residual_stride, feat0, a.feat, n, lane);
+        if (a.residual && 32 * part < n)
+          get_rows<kGated>(res, a.residual, t.row0 + 32 * part, a.residual_stride, feat0, a.feat, n - 32 * part, lane);
       }
       if (sums) {
         ok = ok && __all_sync(0xffffffffu, wait_for(acc_full + buf, (done >> 1) & 1u, gave_up));
         tc_fence_after();
       }
+      auto release = [&] {  // this warp's columns are in registers
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (kPair) arrive_at<false>(acc_empty + buf, 0);
+          else mbar_arrive(acc_empty + buf);
+        }
+      };
       const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTok;
-      for (int c0 = 0; c0 < n; c0 += 32) {
+      if (sums && ok && 32 * part >= n) release();
+      for (int c0 = 32 * part; c0 < n; c0 += 64) {
         float v[2][16];
         if (sums && ok) {
           tmem_load_16x32(acc + c0, v[0]);
           tmem_load_16x32(acc + (16u << 16) + c0, v[1]);
           tmem_load_wait();
-          if (c0 + 32 >= n) {  // all columns are in registers
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (kPair) arrive_at<false>(acc_empty + buf, 0);
-              else mbar_arrive(acc_empty + buf);
-            }
-          }
+          if (c0 + 64 >= n) release();
         } else {
           fill(v, ok ? 0.0f : __int_as_float(0x7fc00000));
         }
@@ -664,8 +679,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kMode, kTok, kGated>::kSplit ?
           uint4 cur[Frag<kGated>::kGroups];
 #pragma unroll
           for (int i = 0; i < Frag<kGated>::kGroups; ++i) cur[i] = res[i];
-          if (kMode == kForward && a.residual && c0 + 32 < n)  // the next chunk's, while this one is worked on
-            get_rows<kGated>(res, a.residual, t.row0 + c0 + 32, a.residual_stride, feat0, a.feat, n - c0 - 32, lane);
+          if (kMode == kForward && a.residual && c0 + 64 < n)  // the next chunk's, while this one is worked on
+            get_rows<kGated>(res, a.residual, t.row0 + c0 + 64, a.residual_stride, feat0, a.feat, n - c0 - 64, lane);
           finish<T, kGated>(a, t, c0, feat0, bias, v, cur, base, 0xffu, lane);
         }
       }
@@ -791,16 +806,18 @@ cudaError_t launch(const char* name, const CUtensorMap& mf, const CUtensorMap& m
                    int64_t grid, int cluster, int tiles_grad_w, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Shape<kMode, kTok, kGated>::kThreads);
   cfg.dynamicSmemBytes = Shape<kMode, kTok, kGated>::kSmem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)cluster;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   Launch guard(name, st);
   return cudaLaunchKernelEx(&cfg, k_product<T, kMode, kTok, kGated>, mf, mt, full, a, tiles_grad_w);
 }

@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "chain.cuh"
 #include "experts.h"
 
 namespace lapsum {
@@ -491,6 +492,8 @@ __device__ __forceinline__ float log_sigmoid(float l) { return fminf(l, 0.0f) - 
 
 template <int kDtype, int kPer, bool kRaw>
 __global__ void __launch_bounds__(kThreads, kPer <= 8 ? 8 : kPer == 16 ? 6 : 3) k_route_fwd(const RouteFwd a) {
+  grid_launch_next();
+  grid_wait_previous();
   __shared__ int all_picked[kWarps][LAPSUM_EXPERTS_MAX_K + 1];
   int* picked = all_picked[threadIdx.x >> 5];
   const int lane = threadIdx.x & 31;
@@ -578,6 +581,8 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? 8 : kPer == 16 ? 6 : 3) 
 template <int kDtype, int kPer>
 __global__ void __launch_bounds__(kThreads) k_route_bwd(const RouteBwd a) {
   const int lane = threadIdx.x & 31;
+  grid_launch_next();
+  grid_wait_previous();
   const bool dense = a.score == LAPSUM_SCORE_SOFTMAX && !a.renormalize;
   for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.tokens; t += (int64_t)gridDim.x * kWarps) {
     const int64_t at = t * a.stride, out = t * a.grad_stride;
@@ -646,13 +651,13 @@ __global__ void __launch_bounds__(kThreads) k_route_bwd(const RouteBwd a) {
 template <int kDtype, int kPer>
 void fwd_as(const RouteFwd& a, unsigned grid, cudaStream_t st) {
   if (!a.bias && (a.groups_kept == a.groups || a.group_top == 1))
-    k_route_fwd<kDtype, kPer, true><<<grid, kThreads, 0, st>>>(a);
+    launch_ex(true, k_route_fwd<kDtype, kPer, true>, dim3(grid), dim3(kThreads), 0, st, a);
   else
-    k_route_fwd<kDtype, kPer, false><<<grid, kThreads, 0, st>>>(a);
+    launch_ex(true, k_route_fwd<kDtype, kPer, false>, dim3(grid), dim3(kThreads), 0, st, a);
 }
 template <int kDtype, int kPer>
 void bwd_as(const RouteBwd& a, unsigned grid, cudaStream_t st) {
-  k_route_bwd<kDtype, kPer><<<grid, kThreads, 0, st>>>(a);
+  launch_ex(true, k_route_bwd<kDtype, kPer>, dim3(grid), dim3(kThreads), 0, st, a);
 }
 
 #define LAPSUM_BY_EXPERTS(fn, dt, ...)             \
