@@ -15,7 +15,8 @@
 //
 // In a block warp 0 fills a ring of stages by tiled copies (64 deep, 128-byte
 // swizzle), warp 1 issues the products, the other four or eight read the
-// accumulators from tensor memory and write the result.  Two accumulators let
+// accumulators from tensor memory and write the result.  (For weight gradients
+// one more warp zeroes the ragged ends.)  Two accumulators let
 // the epilogue of one tile run beside the products of the next; blocks walk
 // the tiles with a stride of the grid.  Three forms, by the rows of an expert:
 //   many   two blocks work as a pair on 256 features x 256 tokens: each copies
@@ -80,7 +81,7 @@ struct Shape {
   static constexpr bool kPair = kTok == 256;
   static constexpr bool kSplit = kTok == 32;       // few rows: clusters, two blocks per SM
   static constexpr int kEpilogue = kSplit ? 4 : 8;  // warps: one or two per quarter of the lanes
-  static constexpr int kThreads = 64 + 32 * kEpilogue;
+  static constexpr int kThreads = 64 + 32 * kEpilogue + (kMode == kGradW ? 32 : 0);
   static constexpr int kFeat = kLanes / (kGated ? 2 : 1);           // features of a block's tile
   static constexpr int kTileFeat = kFeat * (kPair ? 2 : 1);         // of a tile
   static constexpr int kABytes = kLanes * 128;
@@ -434,7 +435,8 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
   uint64_t* acc_full = peer_full + kStages;  // [2]
   uint64_t* acc_empty = acc_full + 2;        // [2]
   uint64_t* drained = acc_empty + 2;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
+  uint64_t* landed = drained + 1;            // kGradW [kStages]: copies of a ragged end
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(landed + kStages);
   volatile uint32_t* gave_up = tmem_at + 1;
   int* table = reinterpret_cast<int*>(tail + 512);
 
@@ -448,6 +450,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
       mbar_init(peer_full + s, 1);
+      mbar_init(landed + s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full + b, 1);
@@ -494,6 +497,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
   if (warp == 0) {
     if (lane == 0) {
       uint32_t s = 0, ph = 0, used = 0;  // stage, its phase, stages filled (at most kStages)
+      uint32_t ends = 0, phases = 0;     // kGradW, a bit per stage: holds a ragged end; its barrier's phase
       bool ok = true;
       for (int tile = first; ok && tile < tiles; tile += step) {
         const Tile t = tile_of<kMode, kTok, kGated>(a, table, tile, half);
@@ -512,25 +516,32 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
           unsigned char* sa = ring + s * S::kStage;
           unsigned char* sb = sa + S::kABytes;
           const int d = c * kDepth;
-          mbar_arrive_expect_tx(full + s, bytes);
+          // a ragged end is full when the zeroing warp says so
+          const bool end = kMode == kGradW && t.n - d < kDepth;
+          uint64_t* bar = end ? landed + s : full + s;
+          if (kMode == kGradW) {
+            ends = end ? ends | 1u << s : ends & ~(1u << s);
+            if (end) phases ^= 1u << s;
+          }
+          mbar_arrive_expect_tx(bar, bytes);
           if (kMode == kForward) {
             if (kGated)
-              tma_load_5d(sa, &map_f, d, 0, 0, t.f0 / 8, t.expert, full + s);
+              tma_load_5d(sa, &map_f, d, 0, 0, t.f0 / 8, t.expert, bar);
             else
-              tma_load_3d(sa, &map_f, d, t.f0, t.expert, full + s);
+              tma_load_3d(sa, &map_f, d, t.f0, t.expert, bar);
           } else if (kMode == kGradX) {
-            tma_load_3d(sa, &map_f, t.f0, d, t.expert, full + s);
-            tma_load_3d(sa + 8192, &map_f, t.f0 + 64, d, t.expert, full + s);
+            tma_load_3d(sa, &map_f, t.f0, d, t.expert, bar);
+            tma_load_3d(sa + 8192, &map_f, t.f0 + 64, d, t.expert, bar);
           } else {
-            tma_load_2d(sa, &map_f, t.f0, t.row0 + d, full + s);
-            tma_load_2d(sa + 8192, &map_f, t.f0 + 64, t.row0 + d, full + s);
+            tma_load_2d(sa, &map_f, t.f0, t.row0 + d, bar);
+            tma_load_2d(sa + 8192, &map_f, t.f0 + 64, t.row0 + d, bar);
           }
-          if (whole) tma_load_2d(sb, &map_full, d, t.row0 + n0, full + s);
+          if (whole) tma_load_2d(sb, &map_full, d, t.row0 + n0, bar);
           for (int b = whole ? boxes : 0; b < boxes; ++b) {
             if (kMode == kGradW)
-              tma_load_2d(sb + b * kBoxBytes, &map_t, t.c0 + n0 + kBox * b, t.row0 + d, full + s);
+              tma_load_2d(sb + b * kBoxBytes, &map_t, t.c0 + n0 + kBox * b, t.row0 + d, bar);
             else
-              tma_load_2d(sb + b * kBoxBytes, &map_t, d, t.row0 + n0 + kBox * b, full + s);
+              tma_load_2d(sb + b * kBoxBytes, &map_t, d, t.row0 + n0 + kBox * b, bar);
           }
           if (used < kStages) ++used;
           if (++s == kStages) {
@@ -545,15 +556,16 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
         for (; used; --used) {
           if (s == 0) ph ^= 1u;
           s = s == 0 ? kStages - 1 : s - 1;
-          mbar_wait_bounded(full + s, ph, kPolls);
+          if (kMode == kGradW && (ends >> s & 1u))
+            mbar_wait_bounded(landed + s, (phases >> s & 1u) ^ 1u, kPolls);
+          else
+            mbar_wait_bounded(full + s, ph, kPolls);
         }
       }
     }
   } else if (warp == 1) {
-    // One lane issues (and, in the second block of a pair, reports its stages);
-    // for weight gradients the warp stays together to zero ragged ends.
-    constexpr bool kWarp = kMode == kGradW;
-    if (kWarp || lane == 0) {
+    // One lane issues and, in the second block of a pair, reports its stages.
+    if (lane == 0) {
       uint32_t s = 0, ph = 0, done = 0;
       bool ok = true;
       int tile = first;
@@ -566,54 +578,38 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
         if (c0 < c1) {
           const uint32_t buf = S::kSplit ? 0u : done & 1u;
           if (half == 0) ok = wait_for(acc_empty + buf, ((S::kSplit ? done : done >> 1) & 1u) ^ 1u, gave_up);
-          if (kWarp) ok = __all_sync(0xffffffffu, ok);
           tc_fence_after();
           const uint32_t acc = tmem + buf * kTok;
           const uint32_t idesc = instr_desc(std::is_same<T, __nv_bfloat16>::value, kMode != kForward, kMode == kGradW,
                                             kLanes * (kPair ? 2 : 1), n);
           for (int c = c0; ok && c < c1; ++c) {
             ok = wait_for(full + s, ph, gave_up);
-            if (kWarp) ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            const uint32_t sa = smem_u32(ring) + s * S::kStage;
             const int left = kMode == kGradW ? cur.n - c * kDepth : kDepth;
-            if (kMode == kGradW && left < kDepth) {
-              // lines of rows behind the expert's last one: zero in both operands
-              // (whatever they held, NaN included, must not reach the sums)
-              const int lines = kDepth - left, blocks = 2 + (own + 63) / 64;
-              for (int i = lane; i < blocks * lines * 8; i += 32) {
-                const int line = i >> 3, blk = line / lines;
-                sts16(sa + blk * 8192 + (left + line - blk * lines) * 128 + (i & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-            if (half != 0) {  // the first block issues for both
-              if (lane == 0) {
-                if (left < kDepth)
-                  arrive_at<true>(peer_full + s, 0);
-                else
-                  arrive_at<false>(peer_full + s, 0);
-              }
+            const bool ragged = left < kDepth;
+            if (half != 0) {
+              if (ragged)
+                arrive_at<true>(peer_full + s, 0);  // with the zeroed lines
+              else
+                arrive_at<false>(peer_full + s, 0);
             } else {
               if (kPair) {
                 ok = wait_for(peer_full + s, ph, gave_up);
-                if (kWarp) ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (left < kDepth) acquire_cluster();
+                if (ok && ragged) mbar_try_wait_cluster(peer_full + s, ph);  // done already: acquires
               }
-              if (lane == 0) {
-                tc_fence_after();
-                const uint64_t da = operand_desc(sa, kMode == kForward ? 16u : 8192u);
-                const uint64_t db = operand_desc(sa + S::kABytes, kMode == kGradW ? 8192u : 16u);
-                constexpr uint32_t kStepA = (kMode == kForward ? 32 : 2048) >> 4,
-                                   kStepB = (kMode == kGradW ? 2048 : 32) >> 4;
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t sa = smem_u32(ring) + s * S::kStage;
+              const uint64_t da = operand_desc(sa, kMode == kForward ? 16u : 8192u);
+              const uint64_t db = operand_desc(sa + S::kABytes, kMode == kGradW ? 8192u : 16u);
+              constexpr uint32_t kStepA = (kMode == kForward ? 32 : 2048) >> 4,
+                                 kStepB = (kMode == kGradW ? 2048 : 32) >> 4;
 #pragma unroll
-                for (uint32_t k = 0; k < kDepth / 16; ++k)
+              for (uint32_t k = 0; k < kDepth / 16; ++k)
+                if (kMode != kGradW || (int)(16 * k) < left)
                   mma_f16<kPair>(acc, da + k * kStepA, db + k * kStepB, idesc, c != c0 || k != 0);
-                mma_commit<kPair>(empty + s);
-                if (c + 1 == c1) mma_commit<kPair>(acc_full + buf);
-              }
+              mma_commit<kPair>(empty + s);
+              if (c + 1 == c1) mma_commit<kPair>(acc_full + buf);
             }
             if (++s == kStages) {
               s = 0;
@@ -626,9 +622,35 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
         if (tile < tiles - step) t = tile_of<kMode, kTok, kGated>(a, table, tile + step, half);
       }
       if (!ok && half == 0) {  // the products in flight end before their tensor memory is freed
-        if (lane == 0) mma_commit<kPair>(drained);
+        mma_commit<kPair>(drained);
         mbar_wait_bounded(drained, 0u, kPolls);
       }
+    }
+  } else if (kMode == kGradW && warp == 2 + S::kEpilogue) {
+    // The products take whole steps of 16 rows: in the last step of an expert
+    // the lines behind its rows are zeroed in both operands (whatever they held,
+    // NaN included, must not reach the sums).  A lane has 16 bytes of one of the
+    // four blocks of 64 columns.
+    uint32_t next = 0, phases = 0;  // the tile's first stage; a parity per stage
+    bool ok = true;
+    for (int tile = first; ok && tile < tiles; tile += step) {
+      const Tile t = tile_of<kMode, kTok, kGated>(a, table, tile, half);
+      next += t.chunks;
+      const int left = t.n & (kDepth - 1);
+      if (left == 0) continue;
+      int n, n0, own;
+      width(t, n, n0, own);
+      const uint32_t s = (next - 1) % kStages;
+      ok = __all_sync(0xffffffffu, wait_for(landed + s, phases >> s & 1u, gave_up));
+      phases ^= 1u << s;
+      if (!ok) break;
+      if ((lane >> 3) < 2 + (own + 63) / 64) {
+        const uint32_t to = smem_u32(ring) + s * S::kStage + (lane >> 3) * 8192 + (lane & 7) * 16;
+        for (int line = left; line & 15; ++line) sts16(to + line * 128, make_uint4(0u, 0u, 0u, 0u));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + s);
     }
   } else if (!S::kSplit) {
     // Two warps share a quarter of the lanes and take every other 32 columns.

@@ -195,7 +195,18 @@ __device__ __forceinline__ void arrive_at(uint64_t* mbar, uint32_t rank) {
   else
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(there) : "memory");
 }
-// its counterpart: what the other block's releasing arrival ordered is visible
-__device__ __forceinline__ void acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// its counterpart, a poll after which what the other block's releasing arrival
+// ordered is visible
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* mbar, uint32_t phase) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(mbar)), "r"(phase)
+      : "memory");
+  return ok != 0u;
+}
 
 }  // namespace lapsum
