@@ -11,7 +11,7 @@ the weights of the choice, at fixed choice.
     w, chosen = ex.route(soft_topk(logits, 8.0, 0.5), 8, score="identity")  # or LapSum memberships
     out = ex.mlp(x, w, chosen, w_in, w_out, activation="swiglu", residual=x)
 
-mlp() is plan, dispatch, linear, linear, combine; each is public.  Like the
+mlp() is plan, dispatch, linear, linear, combine in one; each is public.  Like the
 rest of the package: CUDA tensors only, the current stream of the tensors'
 device, no host synchronisation; every call may be captured into a CUDA graph
 (workspaces are allocated per call, never shared).
@@ -428,21 +428,122 @@ def linear(x, weight, offsets=None, *, bias=None, activation: str | None = None,
                        None if residual is None else _rows16(residual), False, status)[0]
 
 
+def _check_weight(weight, bias, name, x, din, act):
+    _cuda(weight, name, 3, x.device)
+    if weight.dtype != x.dtype:
+        raise TypeError(f"{name} must be {x.dtype}, got {weight.dtype}")
+    e, n, k = weight.shape
+    if k != din:
+        raise ValueError(f"{name} must have {din} inputs, got {k}")
+    if not 1 <= e <= MAX_EXPERTS:
+        raise ValueError(f"{name} must have 1 to {MAX_EXPERTS} experts, got {e}")
+    if k % 8 or n % (16 if act == 4 else 8) or not k or not n:
+        raise ValueError(f"inputs and outputs must be multiples of 8 (outputs of 16 for swiglu), got {k} and {n}")
+    if bias is not None:
+        _cuda(bias, "its bias", 2, x.device)
+        if bias.dtype != x.dtype or tuple(bias.shape) != (e, n):
+            raise ValueError(f"the bias of {name} must be {x.dtype} [{e}, {n}], got {bias.dtype} {tuple(bias.shape)}")
+    return e, n
+
+
+def _mlp_fwd(x, weights, chosen, w_in, w_out, b_in, b_out, act, residual, status, keep):
+    """The layer on laid-out tensors; with keep also what its gradient takes."""
+    p = plan(chosen, w_in.shape[0])
+    t, k = chosen.shape
+    x_rows = _dispatch(x, p.slots, t, k)
+    h, pre = _linear_fwd(x_rows, w_in, p.offsets, b_in, act, None, keep and act != 0, status)
+    y, _ = _linear_fwd(h, w_out, p.offsets, b_out, 0, None, False, status)
+    out = _combine(y, weights, p.rows, residual)
+    return out, (p.offsets, p.rows, p.slots, x_rows, pre, h, y)
+
+
 def mlp(x, weights, chosen, w_in, w_out, *, b_in=None, b_out=None, activation: str | None = "swiglu", residual=None,
         status=None):
     """A layer of experts: every token's weighted sum over its chosen experts of
-    W_out act(W_in x + b_in) + b_out, plus residual.  x [tokens, dim] bf16 or
+    W_out act(W_in x + b_in) + b_out, plus residual: plan, dispatch, linear,
+    linear and combine in one call (and one gradient).  x [tokens, dim] bf16 or
     fp16; weights and chosen [tokens, k] from route(); w_in [experts, hidden
-    (twice for swiglu), dim], w_out [experts, dim_out, hidden]."""
-    p = plan(chosen, w_in.shape[0])
-    h = linear(dispatch(x, p), w_in, p.offsets, bias=b_in, activation=activation, status=status)
-    y = linear(h, w_out, p.offsets, bias=b_out, status=status)
-    return combine(y, weights, p, residual=residual)
+    (twice for swiglu), dim], w_out [experts, dim_out, hidden]; biases
+    [experts, ...]; residual [tokens, dim_out], x itself for instance; status
+    as in linear()."""
+    _cuda(x, "x", 2)
+    _dtype(x, "x", half_only=True)
+    dev = x.device
+    if activation not in _ACTS:
+        raise ValueError(f"activation must be None or one of {sorted(a for a in _ACTS if a)}, got {activation!r}")
+    act = _ACTS[activation]
+    e, up = _check_weight(w_in, b_in, "w_in", x, x.shape[1], act)
+    e2, dim = _check_weight(w_out, b_out, "w_out", x, up // 2 if act == 4 else up, 0)
+    if e != e2:
+        raise ValueError(f"w_in and w_out must have the same experts, got {e} and {e2}")
+    _cuda(chosen, "chosen", 2, dev)
+    chosen = _index(chosen, "chosen", dev)
+    t, k = chosen.shape
+    if t != x.shape[0] or not 1 <= k <= MAX_K:
+        raise ValueError(f"chosen must have x's {x.shape[0]} tokens and 1 to {MAX_K} places, got {tuple(chosen.shape)}")
+    _cuda(weights, "weights", 2, dev)
+    if weights.dtype != _F32 or tuple(weights.shape) != (t, k):
+        raise ValueError(f"weights must be float32 [{t}, {k}], got {weights.dtype} {tuple(weights.shape)}")
+    if residual is not None:
+        _cuda(residual, "residual", 2, dev)
+        if residual.dtype != x.dtype or tuple(residual.shape) != (t, dim):
+            raise ValueError(f"residual must be {x.dtype} [{t}, {dim}], got {residual.dtype} {tuple(residual.shape)}")
+    if status is not None and (_cuda(status, "status", None, dev).dtype != _I32 or status.numel() < 1):
+        raise TypeError("status must be an int32 tensor")
+    if _tracked(x, weights, w_in, w_out, b_in, b_out, residual):
+        own = residual is x  # its gradient joins that of x in one pass
+        return _function("mlp").apply(x, weights, w_in, w_out, b_in, b_out, None if own else residual, own, chosen, act,
+                                      status)
+    return _mlp_fwd(_rows_of(x), weights.contiguous(), chosen, _dense16(w_in), _dense16(w_out),
+                    None if b_in is None else b_in.contiguous(), None if b_out is None else b_out.contiguous(), act,
+                    None if residual is None else _rows_of(residual), status, False)[0]
 
 
 # ---------------------------------------------------------------------------
 # gradients
 # ---------------------------------------------------------------------------
+def _combine_bwd(g, y, weights, rows, slots, need_y, need_w):
+    (t, k), dim = rows.shape, y.shape[1]
+    gy = torch.empty((t * k, dim), dtype=y.dtype, device=y.device) if need_y else None
+    gw = torch.empty_like(weights) if need_w else None
+    if (need_y or need_w) and t * dim:
+        _call("combine_bwd", y.get_device(), g.data_ptr(), _dtype(y, "y"), t, k, dim, _stride(g), y.data_ptr(), _stride(y),
+              weights.data_ptr(), rows.data_ptr(), slots.data_ptr(), _ptr(gy), dim, _ptr(gw))
+    elif gw is not None:
+        gw.zero_()
+    return gy, gw
+
+
+def _linear_bwd(g, x, w, offsets, h, act, need_x, need_w, need_b, status):
+    """(dx, dweight, dbias) for dy = g; h the pre-activation of act != 0."""
+    experts, n, k = w.shape
+    r, dev, dt, index = x.shape[0], x.device, _dtype(x, "x"), x.get_device()
+    gb = torch.empty((experts, n), dtype=x.dtype, device=dev) if need_b else None
+    gx = torch.empty((r, k), dtype=x.dtype, device=dev) if need_x else None
+    gw = torch.empty((experts, n, k), dtype=x.dtype, device=dev) if need_w else None
+    if r == 0:
+        for z in (gb, gw):
+            if z is not None:
+                z.zero_()
+        return gx, gw, gb
+    if need_x or need_w or need_b:
+        gy = gh = _rows16(g)
+        if act or need_b:
+            gh = torch.empty((r, n), dtype=x.dtype, device=dev) if act else None
+            need = int(_load().lapsum_experts_linear_act_workspace_size(r, experts, n)) if need_b else 0
+            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+            _call("linear_act_bwd", index, gy.data_ptr(), dt, r, n, _stride(gy), _ptr(h), n, experts, _ptr(offsets), act,
+                  _ptr(gh), n, _ptr(gb), _ptr(ws), need)
+            gh = gh if act else gy
+        if need_x:
+            _call("linear_dx", index, gh.data_ptr(), dt, r, n, _stride(gh), w.data_ptr(), experts, k, _ptr(offsets),
+                  gx.data_ptr(), k, _ptr(status))
+        if need_w:
+            _call("linear_dweight", index, gh.data_ptr(), dt, r, n, _stride(gh), x.data_ptr(), k, _stride(x), experts,
+                  _ptr(offsets), gw.data_ptr(), _ptr(status))
+    return gx, gw, gb
+
+
 def _make_functions():
     class Route(torch.autograd.Function):
         @staticmethod
@@ -491,15 +592,7 @@ def _make_functions():
             _once()
             y, w, rows, slots = ctx.saved_tensors
             need_y, need_w, need_r = ctx.needs_input_grad[:3]
-            (t, k), dim = rows.shape, y.shape[1]
-            gy = torch.empty((t * k, dim), dtype=y.dtype, device=y.device) if need_y else None
-            gw = torch.empty_like(w) if need_w else None
-            if (need_y or need_w) and t * dim:
-                gg = _rows_of(g)
-                _call("combine_bwd", y.get_device(), gg.data_ptr(), _dtype(y, "y"), t, k, dim, _stride(gg), y.data_ptr(),
-                      _stride(y), w.data_ptr(), rows.data_ptr(), slots.data_ptr(), _ptr(gy), dim, _ptr(gw))
-            elif gw is not None:
-                gw.zero_()
+            gy, gw = _combine_bwd(_rows_of(g), y, w, rows, slots, need_y, need_w)
             return gy, gw, g if need_r else None, None, None
 
     class Linear(torch.autograd.Function):
@@ -518,34 +611,41 @@ def _make_functions():
         def backward(ctx, g):
             _once()
             x, w, offsets, h = ctx.saved_tensors
-            status = ctx.status
             need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
-            experts, n, k = w.shape
-            r, act, dev, dt, index = x.shape[0], ctx.act, x.device, _dtype(x, "x"), x.get_device()
-            gb = torch.empty(ctx.weight_shape[:-1], dtype=x.dtype, device=dev) if need_b else None
-            gx = torch.empty((r, k), dtype=x.dtype, device=dev) if need_x else None
-            gwt = torch.empty(ctx.weight_shape, dtype=x.dtype, device=dev) if need_w else None
-            if r == 0:
-                for z in (gb, gwt):
-                    if z is not None:
-                        z.zero_()
-                return gx, gwt, gb, g if need_r else None, None, None, None
-            if need_x or need_w or need_b:
-                gy = _rows16(g)
-                gh = gy
-                if act or need_b:
-                    gh = torch.empty((r, n), dtype=x.dtype, device=dev) if act else None
-                    need = int(_load().lapsum_experts_linear_act_workspace_size(r, experts, n)) if need_b else 0
-                    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-                    _call("linear_act_bwd", index, gy.data_ptr(), dt, r, n, _stride(gy), _ptr(h), n, experts, _ptr(offsets),
-                          act, _ptr(gh), n, _ptr(gb), _ptr(ws), need)
-                    gh = gh if act else gy
-                if need_x:
-                    _call("linear_dx", index, gh.data_ptr(), dt, r, n, _stride(gh), w.data_ptr(), experts, k, _ptr(offsets),
-                          gx.data_ptr(), k, _ptr(status))
-                if need_w:
-                    _call("linear_dweight", index, gh.data_ptr(), dt, r, n, _stride(gh), x.data_ptr(), k, _stride(x), experts,
-                          _ptr(offsets), gwt.data_ptr(), _ptr(status))
-            return gx, gwt, gb, g if need_r else None, None, None, None
+            gx, gw, gb = _linear_bwd(g, x, w, offsets, h, ctx.act, need_x, need_w, need_b, ctx.status)
+            if gw is not None:
+                gw = gw.view(ctx.weight_shape)
+            if gb is not None:
+                gb = gb.view(ctx.weight_shape[:-1])
+            return gx, gw, gb, g if need_r else None, None, None, None
 
-    _functions.update(route=Route, dispatch=Dispatch, combine=Combine, linear=Linear)
+    class Mlp(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weights, w_in, w_out, b_in, b_out, residual, own, chosen, act, status):
+            x2, w2, wi, wo = _rows_of(x), weights.contiguous(), _dense16(w_in), _dense16(w_out)
+            res = x2 if own else None if residual is None else _rows_of(residual)
+            out, kept = _mlp_fwd(x2, w2, chosen, wi, wo, None if b_in is None else b_in.contiguous(),
+                                 None if b_out is None else b_out.contiguous(), act, res, status, True)
+            ctx.save_for_backward(w2, wi, wo, *kept)
+            ctx.act, ctx.own, ctx.status = act, own, status
+            return out
+
+        @staticmethod
+        def backward(ctx, g):
+            _once()
+            weights, w_in, w_out, offsets, rows, slots, x_rows, pre, h, y = ctx.saved_tensors
+            need_x, need_w, need_in, need_out, need_bi, need_bo, need_r = ctx.needs_input_grad[:7]
+            status = ctx.status
+            inner = need_x or need_in or need_bi
+            g2 = _rows_of(g)
+            gy, gw = _combine_bwd(g2, y, weights, rows, slots, inner or need_out or need_bo, need_w)
+            gx = gwi = gbi = gwo = gbo = None
+            if gy is not None:
+                gh, gwo, gbo = _linear_bwd(gy, h, w_out, offsets, None, 0, inner, need_out, need_bo, status)
+                if inner:
+                    gr, gwi, gbi = _linear_bwd(gh, x_rows, w_in, offsets, pre, ctx.act, need_x, need_in, need_bi, status)
+                    if need_x:
+                        gx = _combine(gr, None, rows, g2 if ctx.own else None)
+            return gx, gw, gwi, gwo, gbi, gbo, g if need_r else None, None, None, None, None
+
+    _functions.update(route=Route, dispatch=Dispatch, combine=Combine, linear=Linear, mlp=Mlp)
