@@ -387,4 +387,96 @@ int lapsum_experts_linear_dweight(const void* grad_h, int dtype, int64_t rows, i
   return done((dtype == LAPSUM_BF16 ? launch_linear_dweight_bf16 : launch_linear_dweight_f16)(p, sms, (cudaStream_t)stream));
 }
 
+// Workspace of the layer: the plan's arrays and scratch, then the rows before,
+// between and after the products, each on a 256-byte boundary.
+struct MlpLayout {
+  size_t offsets, rows, slots, plan, x_rows, h, y, total;
+};
+static MlpLayout mlp_layout(int64_t tokens, int k, int experts, int64_t dim, int64_t hidden, int64_t dim_out) {
+  const size_t n = (size_t)tokens * k;
+  MlpLayout l;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at = (at + bytes + 255) & ~size_t(255);
+    return here;
+  };
+  l.offsets = take(4 * ((size_t)experts + 1));
+  l.rows = take(4 * n);
+  l.slots = take(4 * n);
+  l.plan = take(plan_workspace((int64_t)n, experts));
+  l.x_rows = take(2 * n * dim);
+  l.h = take(2 * n * hidden);
+  l.y = take(2 * n * dim_out);
+  l.total = at;
+  return l;
+}
+static bool mlp_shape(int64_t tokens, int k, int experts, int64_t dim, int64_t hidden, int64_t dim_out) {
+  return tokens >= 1 && k >= 1 && k <= LAPSUM_EXPERTS_MAX_K && tokens <= (kMaxIndex - 1024) / k && experts >= 1 &&
+         experts <= LAPSUM_EXPERTS_MAX && dim >= 1 && hidden >= 1 && dim_out >= 1 && dim <= (1 << 24) &&
+         hidden <= (1 << 24) && dim_out <= (1 << 24);
+}
+
+size_t lapsum_experts_mlp_workspace_size(int64_t tokens, int k, int experts, int64_t dim, int64_t hidden,
+                                         int64_t dim_out) {
+  if (!mlp_shape(tokens, k, experts, dim, hidden, dim_out)) return 0;
+  return mlp_layout(tokens, k, experts, dim, hidden, dim_out).total;
+}
+
+int lapsum_experts_mlp_fwd(const void* x, int dtype, int64_t tokens, int64_t dim, int64_t x_stride, const float* weights,
+                           const int32_t* chosen, int k, const void* w_in, const void* b_in, int experts, int64_t up,
+                           int activation, const void* w_out, const void* b_out, int64_t dim_out, const void* residual,
+                           int64_t residual_stride, void* out, int64_t out_stride, uint32_t* status, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  const bool gated = activation == LAPSUM_ACT_SWIGLU;
+  if (activation < LAPSUM_ACT_NONE || activation > LAPSUM_ACT_SWIGLU || up < 1 || (gated && up % 16)) return LAPSUM_EINVAL;
+  const int64_t hidden = gated ? up / 2 : up;
+  if (!mlp_shape(tokens, k, experts, dim, hidden, dim_out)) return LAPSUM_EINVAL;
+  const int64_t n = tokens * k;
+  // everything that a later step could refuse is checked before the first is enqueued
+  if (!linear_shape(dtype, n, dim, up) || !linear_shape(dtype, n, hidden, dim_out)) return LAPSUM_EINVAL;
+  if (!tiles_fit(n, experts, dim, up) || !tiles_fit(n, experts, hidden, dim_out)) return LAPSUM_ETOOLARGE;
+  if (!x || !weights || !chosen || !w_in || !w_out || !out || x_stride < dim || out_stride < dim_out ||
+      (residual && residual_stride < dim_out))
+    return LAPSUM_EINVAL;
+  if (!aligned(x, 2) || !aligned(out, 2) || !aligned(residual, 2) || !aligned(weights, 4) || !aligned(chosen, 4) ||
+      !aligned(w_in, 16) || !aligned(w_out, 16) || !aligned(b_in, 2) || !aligned(b_out, 2) || !aligned(status, 4))
+    return LAPSUM_EINVAL;
+  const MlpLayout l = mlp_layout(tokens, k, experts, dim, hidden, dim_out);
+  if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256)) return LAPSUM_EWORKSPACE;
+  struct {
+    const void* p;
+    size_t n;
+  } outs[2] = {{out, span(tokens, dim_out, out_stride, 2)}, {workspace, l.total}},
+    ins[8] = {{x, span(tokens, dim, x_stride, 2)},
+              {weights, 4 * (size_t)n},
+              {chosen, 4 * (size_t)n},
+              {w_in, 2 * (size_t)experts * up * dim},
+              {b_in, 2 * (size_t)experts * up},
+              {w_out, 2 * (size_t)experts * dim_out * hidden},
+              {b_out, 2 * (size_t)experts * dim_out},
+              {residual, span(tokens, dim_out, residual_stride, 2)}};
+  for (const auto& o : outs)
+    for (const auto& i : ins)
+      if (overlaps(o.p, o.n, i.p, i.n)) return LAPSUM_EINVAL;
+  if (overlaps(outs[0].p, outs[0].n, outs[1].p, outs[1].n)) return LAPSUM_EINVAL;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  auto* offsets = reinterpret_cast<int32_t*>(ws + l.offsets);
+  auto* rows = reinterpret_cast<int32_t*>(ws + l.rows);
+  auto* slots = reinterpret_cast<int32_t*>(ws + l.slots);
+  int rc = lapsum_experts_plan(chosen, n, experts, offsets, rows, slots, ws + l.plan, l.x_rows - l.plan, stream);
+  if (rc == LAPSUM_OK)
+    rc = lapsum_experts_dispatch(x, dtype, tokens, k, dim, x_stride, slots, ws + l.x_rows, dim, stream);
+  if (rc == LAPSUM_OK)
+    rc = lapsum_experts_linear_fwd(ws + l.x_rows, dtype, n, dim, dim, w_in, experts, up, offsets, b_in, activation,
+                                   nullptr, 0, ws + l.h, hidden, nullptr, 0, status, stream);
+  if (rc == LAPSUM_OK)
+    rc = lapsum_experts_linear_fwd(ws + l.h, dtype, n, hidden, hidden, w_out, experts, dim_out, offsets, b_out,
+                                   LAPSUM_ACT_NONE, nullptr, 0, ws + l.y, dim_out, nullptr, 0, status, stream);
+  if (rc == LAPSUM_OK)
+    rc = lapsum_experts_combine(ws + l.y, dtype, tokens, k, dim_out, dim_out, weights, rows, residual, residual_stride,
+                                out, out_stride, stream);
+  return rc;
+}
+
 }  // extern "C"

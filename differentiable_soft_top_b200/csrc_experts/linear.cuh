@@ -87,10 +87,10 @@ struct Shape {
   static constexpr int kABytes = kLanes * 128;
   static constexpr int kBBytes = (kPair ? kTok / 2 : kTok) * 128;
   static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kBudget = kSplit ? 100 * 1024 : 196 * 1024;
-  static constexpr int kStages = kBudget / kStage;
+  static constexpr int kStages = kSplit ? 4 : 196 * 1024 / kStage;
   static constexpr int kTmemCols = kSplit ? 32 : 2 * kTok;
-  static constexpr int kStaging = kSplit ? 0 : kEpilogue * 32 * kPitch;  // the split form stages in the ring
+  // (the split form stages in the ring; here its ranks' partials arrive)
+  static constexpr int kStaging = kSplit ? 32 * kLanes * 4 : kEpilogue * 32 * kPitch;
   static constexpr int kTable = kMode == kGradW ? 0 : (LAPSUM_EXPERTS_MAX + 2) * 4;
   static constexpr int kSmem = kStages * kStage + kStaging + kTable + 1024 /* alignment */ + 512 /* barriers */;
 };
@@ -441,6 +441,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
   int* table = reinterpret_cast<int*>(tail + 512);
 
   grid_launch_next();
+  if (S::kSplit) cluster_arrive();  // waited for before the first access to another block's memory
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = kPair ? (int)cluster_rank() : 0;
   if (threadIdx.x == 0) {
@@ -713,6 +714,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
   if constexpr (S::kSplit) {
     // one tile per cluster: the ranks' partials meet in shared memory
     __syncwarp();
+    cluster_wait();  // every block has started
     const bool busy = first < tiles;  // the same for all ranks of the cluster
     if (busy) {
       const Tile t = tile_of<kMode, kTok, kGated>(a, table, first, 0);
@@ -723,8 +725,13 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
       float v[2][16], bias[4];
       uint4 res[Frag<kGated>::kGroups];
       // every product has read its operands (acc_full), so the ring is free
-      float* red = reinterpret_cast<float*>(ring) + quarter * 1024 + lane;  // [warp][value][lane]
-      const uint32_t base = smem_u32(ring) + 16384 + quarter * 32 * kPitch;
+      const uint32_t base = smem_u32(ring) + quarter * 32 * kPitch;
+      // A piece is 8 tokens x 16 lanes (4 values of a thread), piece p the one of
+      // tokens 8 (p / 2) .. and lanes 16 (p % 2) ..; rank p % ranks joins it.
+      // partials[rank][value][thread], 32 values in all: each rank sends the
+      // pieces of the others to where they are joined.
+      const uint32_t partials = smem_u32(staging) + ((quarter << 5) + lane) * 4;
+      const int each = 32 / ranks;
       bool ok = true;
       if (warp >= 2) {
         load_bias<T, kGated>(a, t, feat0, bias, lane);
@@ -743,32 +750,33 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
         }
         if (ranks > 1) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (8 * ((i & 15) >> 2) < t.n) red[32 * i] = v[i >> 4][i & 15];
+          for (int p = 0; p < 8; ++p)
+            if (8 * (p >> 1) < t.n) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                cluster_store(partials + (rank * each + p / ranks * 4 + i) * (kLanes * 4), p & (ranks - 1),
+                              v[p & 1][4 * (p >> 1) + i]);
+            }
         }
       }
       uint32_t own = 0xffu;
       if (ranks > 1) {
         __syncwarp();
-        cluster_sync();
-        // this rank finishes every ranks-th piece of 8 tokens x 16 lanes
+        cluster_sync();  // nothing goes between the blocks after this
         own = ranks == 8 ? 1u << rank : ranks == 4 ? 0x11u << rank : 0x55u << rank;
         if (warp >= 2) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int j = (i & 15) >> 2, h = i >> 4;
-            float sum = 0.0f;
-            if (8 * j < t.n && (own >> (2 * j + h) & 1u))
-              for (int q = 0; q < ranks; ++q) sum += cluster_load(smem_u32(red + 32 * i), q);
-            v[h][i & 15] = sum;
-          }
+          for (int p = 0; p < 8; ++p)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float sum = 0.0f;
+              if (8 * (p >> 1) < t.n && (own >> p & 1u))
+                for (int q = 0; q < ranks; ++q) sum += lds4(partials + (q * each + p / ranks * 4 + i) * (kLanes * 4));
+              v[p & 1][4 * (p >> 1) + i] = sum;
+            }
         }
       }
       if (warp >= 2) finish<T, kGated>(a, t, 0, feat0, bias, v, res, base, own, lane);
-      if (ranks > 1) {
-        __syncwarp();
-        cluster_sync();  // no block leaves while another reads its partials
-      }
     }
   }
 

@@ -80,6 +80,7 @@ def _load():
                 "linear_act_bwd": [P, i32, i64, i64, i64, P, i64, i32, P, i32, P, i64, P, P, sz, P],
                 "linear_dx": [P, i32, i64, i64, i64, P, i32, i64, P, P, i64, P, P],
                 "linear_dweight": [P, i32, i64, i64, i64, P, i64, i64, i32, P, P, P, P],
+                "mlp_fwd": [P, i32, i64, i64, i64, P, P, i32, P, P, i32, i64, i32, P, P, i64, P, i64, P, i64, P, P, sz, P],
                 "trace_collect": [ctypes.c_char_p, sz],
             }.items():
                 fn = getattr(lib, "lapsum_experts_" + name)
@@ -88,6 +89,8 @@ def _load():
             lib.lapsum_experts_plan_workspace_size.restype = sz
             lib.lapsum_experts_linear_act_workspace_size.argtypes = [i64, i32, i64]
             lib.lapsum_experts_linear_act_workspace_size.restype = sz
+            lib.lapsum_experts_mlp_workspace_size.argtypes = [i64, i32, i32, i64, i64, i64]
+            lib.lapsum_experts_mlp_workspace_size.restype = sz
             lib.lapsum_experts_last_cuda_error.argtypes = []
             lib.lapsum_experts_last_cuda_error.restype = ctypes.c_char_p
             lib.lapsum_experts_launch_count.argtypes = []
@@ -446,12 +449,12 @@ def _check_weight(weight, bias, name, x, din, act):
     return e, n
 
 
-def _mlp_fwd(x, weights, chosen, w_in, w_out, b_in, b_out, act, residual, status, keep):
-    """The layer on laid-out tensors; with keep also what its gradient takes."""
+def _mlp_fwd(x, weights, chosen, w_in, w_out, b_in, b_out, act, residual, status):
+    """The layer on laid-out tensors, and what its gradient takes."""
     p = plan(chosen, w_in.shape[0])
     t, k = chosen.shape
     x_rows = _dispatch(x, p.slots, t, k)
-    h, pre = _linear_fwd(x_rows, w_in, p.offsets, b_in, act, None, keep and act != 0, status)
+    h, pre = _linear_fwd(x_rows, w_in, p.offsets, b_in, act, None, act != 0, status)
     y, _ = _linear_fwd(h, w_out, p.offsets, b_out, 0, None, False, status)
     out = _combine(y, weights, p.rows, residual)
     return out, (p.offsets, p.rows, p.slots, x_rows, pre, h, y)
@@ -494,9 +497,20 @@ def mlp(x, weights, chosen, w_in, w_out, *, b_in=None, b_out=None, activation: s
         own = residual is x  # its gradient joins that of x in one pass
         return _function("mlp").apply(x, weights, w_in, w_out, b_in, b_out, None if own else residual, own, chosen, act,
                                       status)
-    return _mlp_fwd(_rows_of(x), weights.contiguous(), chosen, _dense16(w_in), _dense16(w_out),
-                    None if b_in is None else b_in.contiguous(), None if b_out is None else b_out.contiguous(), act,
-                    None if residual is None else _rows_of(residual), status, False)[0]
+    out = torch.empty((t, dim), dtype=x.dtype, device=dev)
+    if t == 0:
+        return out
+    x, w_in, w_out, weights = _rows_of(x), _dense16(w_in), _dense16(w_out), weights.contiguous()
+    b_in = None if b_in is None else b_in.contiguous()
+    b_out = None if b_out is None else b_out.contiguous()
+    residual = None if residual is None else _rows_of(residual)
+    need = _load().lapsum_experts_mlp_workspace_size(t, k, e, x.shape[1], w_out.shape[2], dim)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _call("mlp_fwd", x.get_device(), x.data_ptr(), _DTYPES[x.dtype], t, x.shape[1], _stride(x), weights.data_ptr(),
+          chosen.data_ptr(), k, w_in.data_ptr(), _ptr(b_in), e, up, act, w_out.data_ptr(), _ptr(b_out), dim,
+          _ptr(residual), _stride(residual) if residual is not None else 0, out.data_ptr(), dim, _ptr(status),
+          ws.data_ptr(), need)
+    return out
 
 
 # ---------------------------------------------------------------------------
@@ -625,7 +639,7 @@ def _make_functions():
             x2, w2, wi, wo = _rows_of(x), weights.contiguous(), _dense16(w_in), _dense16(w_out)
             res = x2 if own else None if residual is None else _rows_of(residual)
             out, kept = _mlp_fwd(x2, w2, chosen, wi, wo, None if b_in is None else b_in.contiguous(),
-                                 None if b_out is None else b_out.contiguous(), act, res, status, True)
+                                 None if b_out is None else b_out.contiguous(), act, res, status)
             ctx.save_for_backward(w2, wi, wo, *kept)
             ctx.act, ctx.own, ctx.status = act, own, status
             return out

@@ -215,6 +215,24 @@ LAPSUM_API int lapsum_experts_linear_dweight(const void* grad_h, int dtype, int6
                                              int experts, const int32_t* offsets, void* grad_weight,
                                              uint32_t* status, void* stream);
 
+/*
+ * The layer in one call (forward only): plan, dispatch, product with bias and
+ * activation, product with bias, weighted sum with residual, each as above,
+ * for x [tokens, dim] (bf16 or fp16), chosen and weights [tokens, k], w_in
+ * [experts, up, dim] (up = hidden, or 2 hidden for LAPSUM_ACT_SWIGLU), w_out
+ * [experts, dim_out, hidden] and out [tokens, dim_out].  What lies between is in
+ * the workspace (lapsum_experts_mlp_workspace_size bytes, 256-byte aligned).
+ * x, residual and out have any row stride; the rest is contiguous.
+ */
+LAPSUM_API size_t lapsum_experts_mlp_workspace_size(int64_t tokens, int k, int experts, int64_t dim, int64_t hidden,
+                                                    int64_t dim_out);
+LAPSUM_API int lapsum_experts_mlp_fwd(const void* x, int dtype, int64_t tokens, int64_t dim, int64_t x_stride,
+                                      const float* weights, const int32_t* chosen, int k, const void* w_in,
+                                      const void* b_in, int experts, int64_t up, int activation, const void* w_out,
+                                      const void* b_out, int64_t dim_out, const void* residual,
+                                      int64_t residual_stride, void* out, int64_t out_stride, uint32_t* status,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
 /* Text of the CUDA error behind the last LAPSUM_ECUDA that this library
    returned on the calling host thread. */
 LAPSUM_API const char* lapsum_experts_last_cuda_error(void);

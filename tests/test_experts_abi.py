@@ -155,6 +155,25 @@ def test_products_reject_bad_arguments(lib):
     ])
 
 
+def test_layer_rejects_bad_arguments(lib):
+    names = "x dtype tokens dim xs w chosen k wi bi experts up act wo bo dim_out res rs out os status ws wsb stream".split()
+    good = dict(x=at(0), dtype=1, tokens=8, dim=64, xs=64, w=at(1), chosen=at(2), k=2, wi=at(3), bi=at(4), experts=4, up=128,
+                act=4, wo=at(5), bo=at(6), dim_out=72, res=at(7), rs=72, out=at(8), os=72, status=at(9), ws=at(10), wsb=1 << 20,
+                stream=None)
+    need = lib.lapsum_experts_mlp_workspace_size(8, 2, 4, 64, 64, 72)
+    assert need >= 16 * 2 * (64 + 64 + 72)
+    assert lib.lapsum_experts_mlp_workspace_size(0, 2, 4, 64, 64, 72) == 0
+    assert lib.lapsum_experts_mlp_workspace_size(8, 33, 4, 64, 64, 72) == 0
+    refused(lib.lapsum_experts_mlp_fwd, names, good, [
+        (dict(x=None), EINVAL), (dict(w=None), EINVAL), (dict(chosen=None), EINVAL), (dict(wi=None), EINVAL),
+        (dict(wo=None), EINVAL), (dict(out=None), EINVAL), (dict(dtype=0), EINVAL), (dict(tokens=0), EINVAL), (dict(k=0), EINVAL),
+        (dict(k=33), EINVAL), (dict(dim=60), EINVAL), (dict(xs=56), EINVAL), (dict(up=120), EINVAL), (dict(act=0, up=100), EINVAL),
+        (dict(act=7), EINVAL), (dict(dim_out=70), EINVAL), (dict(os=64), EINVAL), (dict(rs=64), EINVAL), (dict(experts=0), EINVAL),
+        (dict(experts=1025), EINVAL), (dict(wi=at(3) + 8), EINVAL), (dict(out=at(0)), EINVAL), (dict(out=at(10) + 256), EINVAL),
+        (dict(ws=at(5)), EINVAL), (dict(ws=None), EWORKSPACE), (dict(wsb=need - 1), EWORKSPACE), (dict(ws=at(10) + 16), EWORKSPACE),
+    ])
+
+
 def test_binding_refuses_cpu_tensors_and_bad_types():
     torch = pytest.importorskip("torch")
     x, c = torch.zeros(4, 16), torch.zeros(4, 2, dtype=torch.int32)
