@@ -57,6 +57,7 @@ constexpr int kDepth = 64;              // contraction per stage: one 128-byte l
 constexpr int kLanes = 128;             // accumulator lanes of a block
 constexpr int kTokBox = 32;             // tokens per copied box of a ragged tile (a full one: one box)
 constexpr uint32_t kPolls = 1u << 22;   // polls of a bounded wait, about a second
+constexpr int kGroup = 16;              // token tiles that share their features' tiles in time
 constexpr int kPitch = 80;              // bytes between staged rows of 64: conflict-free
 
 struct Args {
@@ -191,9 +192,8 @@ __device__ __forceinline__ Tile tile_of(const Args& a, const int* table, int til
     t.chunks = (t.n + kDepth - 1) / kDepth;
     return t;
   }
-  const int tt = tile / ftiles;
-  t.f0 = (tile - tt * ftiles) * S::kTileFeat + half * S::kFeat;
   int lo = 0, hi = a.experts;  // the last expert whose first tile is <= tt
+  const int tt = tile / ftiles;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (table[mid] <= tt) lo = mid; else hi = mid - 1;
@@ -201,7 +201,14 @@ __device__ __forceinline__ Tile tile_of(const Args& a, const int* table, int til
   t.expert = lo;
   int row0, n;
   row_range(a, lo, row0, n);
-  const int skip = (tt - table[lo]) * kTok;
+  // An expert's tiles go in groups of up to kGroup token tiles, each feature
+  // tile of the group's next to one another: what runs at one time then reads
+  // about as many rows of the weights as of the tokens, not all of the weights.
+  const int in = tile - table[lo] * ftiles, count = table[lo + 1] - table[lo];
+  const int group = in / (kGroup * ftiles), wide = min(kGroup, count - group * kGroup);
+  const int rest = in - group * kGroup * ftiles, f = rest / wide;
+  t.f0 = f * S::kTileFeat + half * S::kFeat;
+  const int skip = (group * kGroup + rest - f * wide) * kTok;
   t.row0 = row0 + skip;
   t.n = min(n - skip, kTok);
   t.chunks = lo < a.experts ? (a.depth + kDepth - 1) / kDepth : 0;

@@ -9,9 +9,9 @@
 //
 // Equal results whatever the rounding: fp32 keys, their last 5 bits replaced by
 // the place in the lane, decide only when neighbours in the order lie further
-// apart than that and the fp32 error can reach, or are truly equal; a token
-// where they do not is done again with fp64 keys (less than 1 in 100 at 256
-// experts).  Without a bias and without sums of two keys the order of the keys
+// apart than that and the fp32 error can reach, or are truly equal.  Where they
+// do not (about 1 token in 50 at 256 sigmoid scores) the candidates are put in
+// order by fp64 keys; where that does not settle it, all experts are.  Without a bias and without sums of two keys the order of the keys
 // is the order of the scores, which 16-bit scores show exactly.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -234,6 +234,11 @@ __device__ __forceinline__ bool keep_groups(const Rule& r, const Keys& in, const
   return certain;
 }
 
+template <int kDtype, int kPer>
+__device__ __noinline__ uint32_t groups_again(Rule r, Keys in);
+template <int kDtype, int kPer>
+__device__ __noinline__ bool order_again(Rule r, Keys in, int* picked, int count);
+
 // o in descending order (Batcher's odd-even merge sort)
 template <int N>
 __device__ __forceinline__ void sort_down(uint32_t (&o)[N]) {
@@ -253,8 +258,8 @@ __device__ __forceinline__ void sort_down(uint32_t (&o)[N]) {
 }
 
 // Lane j < k gets the token's j-th choice (or -1) in `mine`.  l: this lane's
-// scores, -inf where masked; b: its biases; picked: k + 1 places in shared
-// memory.  False where fp32 keys cannot tell.
+// scores, -inf where masked; b: its biases; picked: k + 2 places in shared
+// memory.  False where neither fp32 keys nor fp64 keys of the highest can tell.
 template <int kDtype, int kPer, bool kRaw>
 __device__ __forceinline__ bool choose(const Rule& r, const Keys& in, const float (&l)[kPer], const float (&b)[kPer],
                                        int* picked, int& mine) {
@@ -262,7 +267,16 @@ __device__ __forceinline__ bool choose(const Rule& r, const Keys& in, const floa
   uint32_t o[kPer];
   keys_of<float, kRaw>(r, in, l, b, o);
   bool certain = true;
-  if (r.kept < r.groups) certain = keep_groups<float, !kRaw>(r, in, l, o);
+  if (r.kept < r.groups) {
+    const bool sure = keep_groups<float, !kRaw>(r, in, l, o);
+    if constexpr (!kRaw)
+      if (!sure) {
+        const uint32_t stay = groups_again<kDtype, kPer>(r, in);
+        keys_of<float, kRaw>(r, in, l, b, o);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) o[i] = stay >> i & 1u ? o[i] : 0u;
+      }
+  }
   // exact: the bits that make room for the place in the lane were 0 anyway
   bool exact = kRaw;
   if (kRaw && kDtype == LAPSUM_F32) {
@@ -275,18 +289,21 @@ __device__ __forceinline__ bool choose(const Rule& r, const Keys& in, const floa
   for (int i = 0; i < kPer; ++i) o[i] = (o[i] & ~31u) | (31u - i);  // below 32: nothing there
   sort_down(o);
   const int rounds = exact ? r.k : r.k + 1;  // with the choice that would follow
-  for (int j = lane; j <= r.k; j += 32) picked[j] = -1;
+  for (int j = lane; j <= r.k + 1; j += 32) picked[j] = -1;
   __syncwarp();
-  for (int j = 0; j < rounds; ++j) {
+  auto pick = [&](int j) {  // false: nothing left
     const uint32_t head = o[0] & ~31u, m = __reduce_max_sync(kAll, head);
-    if (m == 0) break;  // nothing left
+    if (m == 0) return false;
     // equal keys: the lowest lane, in it the lowest place
     const bool win = lane == __ffs(__ballot_sync(kAll, head == m)) - 1;
     if (win) picked[j] = lane * kPer + 31 - (int)(o[0] & 31u);
 #pragma unroll
     for (int i = 0; i + 1 < kPer; ++i) o[i] = win ? o[i + 1] : o[i];
     o[kPer - 1] = win ? 0u : o[kPer - 1];
-  }
+    return true;
+  };
+  bool more = true;
+  for (int j = 0; more && j < rounds; ++j) more = pick(j);
   __syncwarp();
   mine = lane < r.k ? picked[lane] : -1;
   if (!exact) {
@@ -325,6 +342,12 @@ __device__ __forceinline__ bool choose(const Rule& r, const Keys& in, const floa
       if (!(key - key1 > bound) && !same) certain = false;
     }
     certain = __all_sync(kAll, certain);
+    if (!kRaw && !certain && r.k + 2 <= 32) {  // put the candidates and one more in order by their fp64 keys
+      const int count = more && pick(r.k + 1) ? r.k + 2 : r.k + 1;
+      __syncwarp();
+      certain = order_again<kDtype, kPer>(r, in, picked, count);
+      mine = lane < r.k ? picked[lane] : -1;
+    }
   }
   __syncwarp();
   return certain;
@@ -467,6 +490,74 @@ __device__ __forceinline__ void load_token(const void* scores, int64_t at, int e
   load_scores<kDtype, kPer>(scores, at + e0, max(0, min(kPer, experts - e0)), vec, l);
 }
 
+// Which of this lane's experts are in groups that stay, by fp64 keys.
+template <int kDtype, int kPer>
+__device__ __noinline__ uint32_t groups_again(Rule r, Keys in) {
+  float l[kPer], b[kPer];
+  load_token<kDtype, kPer>(in.scores, in.at, r.experts, false, l);
+  load_biases<kPer>(in.bias, r.experts, false, b);
+  mask_token<true>(l, b);
+  uint64_t o[kPer];
+  if (r.raw)
+    keys_of<double, true>(r, in, l, b, o);
+  else
+    keys_of<double, false>(r, in, l, b, o);
+  keep_groups<double, false>(r, in, l, o);
+  uint32_t stay = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) stay |= o[i] ? 1u << i : 0u;
+  return stay;
+}
+
+// Puts the count candidates in picked[] (the highest fp32 keys, at most 32) in
+// the order of their fp64 keys.  False when an expert that is not among them
+// could belong to the first k: the last candidate, above whose fp32 key none of
+// the others lies, is too near the k-th.
+template <int kDtype, int kPer>
+__device__ __noinline__ bool order_again(Rule r, Keys in, int* picked, int count) {
+  const int lane = threadIdx.x & 31;
+  double total = 1.0;
+  if (!r.raw && r.score == LAPSUM_SCORE_SOFTMAX) {
+    float l[kPer], b[kPer];
+    load_token<kDtype, kPer>(in.scores, in.at, r.experts, false, l);
+    load_biases<kPer>(in.bias, r.experts, false, b);
+    mask_token<true>(l, b);
+    total = 0.0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (l[i] != -INFINITY) total += exp((double)l[i] - (double)in.top);
+    total = warp_sum(total);
+  }
+  int e = lane < count ? picked[lane] : -1;
+  count = __popc(__ballot_sync(kAll, e >= 0));
+  double key = -INFINITY, s = 0.0;
+  if (e >= 0) {
+    s = (double)load_score<kDtype>(in.scores, in.at + e);
+    if (!r.raw) {
+      if (r.score == LAPSUM_SCORE_SOFTMAX) s = exp(s - (double)in.top) * (1.0 / total);
+      if (r.score == LAPSUM_SCORE_SIGMOID) s = 1.0 / (1.0 + exp(-s));
+    }
+    key = s + (in.bias ? (double)__ldg(in.bias + e) : 0.0);
+  }
+  int rank = 0;
+  for (int j = 0; j < count; ++j) {
+    const double other = __shfl_sync(kAll, key, j);
+    const int oe = __shfl_sync(kAll, e, j);
+    rank += (other > key || (other == key && oe < e)) ? 1 : 0;
+  }
+  bool certain = true;
+  if (count == r.k + 2) {
+    const int kth = __ffs(__ballot_sync(kAll, e >= 0 && rank == r.k - 1)) - 1;
+    const double low = __shfl_sync(kAll, key, kth);
+    const double last = __shfl_sync(kAll, key, count - 1), last_s = __shfl_sync(kAll, s, count - 1);
+    certain = low - last > 1e-5 * fabs(last) + 1.6e-5 * fabs(last_s) + 1e-37;
+  }
+  __syncwarp();
+  if (e >= 0) picked[rank] = e;
+  __syncwarp();
+  return certain;
+}
+
 // The choice of a token whose fp32 keys lie too close.
 template <int kDtype, int kPer>
 __device__ __noinline__ int choose_again(Rule r, Keys in, int* picked) {
@@ -494,7 +585,7 @@ template <int kDtype, int kPer, bool kRaw>
 __global__ void __launch_bounds__(kThreads, kPer <= 8 ? 8 : kPer == 16 ? 6 : 3) k_route_fwd(const RouteFwd a) {
   grid_launch_next();
   grid_wait_previous();
-  __shared__ int all_picked[kWarps][LAPSUM_EXPERTS_MAX_K + 1];
+  __shared__ int all_picked[kWarps][LAPSUM_EXPERTS_MAX_K + 2];
   int* picked = all_picked[threadIdx.x >> 5];
   const int lane = threadIdx.x & 31;
   Rule r;
