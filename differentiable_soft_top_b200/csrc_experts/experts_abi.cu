@@ -387,6 +387,67 @@ int lapsum_experts_linear_dweight(const void* grad_h, int dtype, int64_t rows, i
   return done((dtype == LAPSUM_BF16 ? launch_linear_dweight_bf16 : launch_linear_dweight_f16)(p, sms, (cudaStream_t)stream));
 }
 
+static size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+
+size_t lapsum_experts_linear_bwd_workspace_size(int64_t rows, int experts, int64_t out, int activation, int with_bias) {
+  if (rows < 1 || experts < 1 || experts > LAPSUM_EXPERTS_MAX || out < 1) return 0;
+  return (activation != LAPSUM_ACT_NONE ? round256(2 * (size_t)rows * out) : 0) +
+         (with_bias ? act_bwd_workspace(rows, experts, out) : 0);
+}
+
+int lapsum_experts_linear_bwd(const void* grad_y, int dtype, int64_t rows, int64_t out, int64_t grad_y_stride,
+                              const void* preact, const void* x, int64_t in, int64_t x_stride, const void* weight,
+                              int experts, const int32_t* offsets, int activation, void* grad_x, void* grad_weight,
+                              void* grad_bias, uint32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
+  // everything that a later step could refuse is checked before the first is enqueued
+  if (!linear_shape(dtype, rows, in, out) || !experts_shape(experts, offsets)) return LAPSUM_EINVAL;
+  if (activation < LAPSUM_ACT_NONE || activation > LAPSUM_ACT_SWIGLU) return LAPSUM_EINVAL;
+  const bool gated = activation == LAPSUM_ACT_SWIGLU, plain = activation == LAPSUM_ACT_NONE;
+  if (gated && out % 16) return LAPSUM_EINVAL;
+  if (!tiles_fit(rows, experts, in, out)) return LAPSUM_ETOOLARGE;
+  if (!grad_x && !grad_weight && !grad_bias) return LAPSUM_EINVAL;
+  const int64_t width = gated ? out / 2 : out;
+  if (!matrix16(grad_y, width, grad_y_stride) || (!plain && !matrix16(preact, out, out)) || !aligned(grad_bias, 2) ||
+      !aligned(status, 4))
+    return LAPSUM_EINVAL;
+  if ((grad_x && (!matrix16(grad_x, in, in) || !weight || !aligned(weight, 16))) ||
+      (grad_weight && (!aligned(grad_weight, 16) || !matrix16(x, in, x_stride))))
+    return LAPSUM_EINVAL;
+  const size_t need = lapsum_experts_linear_bwd_workspace_size(rows, experts, out, activation, grad_bias != nullptr);
+  if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return LAPSUM_EWORKSPACE;
+  const size_t wn = 2 * (size_t)experts * out * in;
+  struct {
+    const void* p;
+    size_t n;
+  } outs[4] = {{grad_x, span(rows, in, in, 2)}, {grad_weight, wn}, {grad_bias, 2 * (size_t)experts * out}, {workspace, need}},
+    ins[5] = {{grad_y, span(rows, width, grad_y_stride, 2)},
+              {plain ? nullptr : preact, span(rows, out, out, 2)},
+              {grad_weight ? x : nullptr, span(rows, in, x_stride, 2)},
+              {grad_x ? weight : nullptr, wn},
+              {offsets, 4 * (size_t)(experts + 1)}};
+  for (int o = 0; o < 4; ++o) {
+    for (const auto& i : ins)
+      if (overlaps(outs[o].p, outs[o].n, i.p, i.n)) return LAPSUM_EINVAL;
+    for (int q = 0; q < o; ++q)
+      if (overlaps(outs[o].p, outs[o].n, outs[q].p, outs[q].n)) return LAPSUM_EINVAL;
+  }
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  const size_t gh_bytes = plain ? 0 : round256(2 * (size_t)rows * out);
+  const void* gh = plain ? grad_y : ws;
+  const int64_t gh_stride = plain ? grad_y_stride : out;
+  int rc = LAPSUM_OK;
+  if (!plain || grad_bias)
+    rc = lapsum_experts_linear_act_bwd(grad_y, dtype, rows, out, grad_y_stride, preact, out, experts, offsets, activation,
+                                       plain ? nullptr : ws, out, grad_bias, ws + gh_bytes, workspace_bytes - gh_bytes,
+                                       stream);
+  if (rc == LAPSUM_OK && grad_x)
+    rc = lapsum_experts_linear_dx(gh, dtype, rows, out, gh_stride, weight, experts, in, offsets, grad_x, in, status, stream);
+  if (rc == LAPSUM_OK && grad_weight)
+    rc = lapsum_experts_linear_dweight(gh, dtype, rows, out, gh_stride, x, in, x_stride, experts, offsets, grad_weight,
+                                       status, stream);
+  return rc;
+}
+
 // Workspace of the layer: the plan's arrays and scratch, then the rows before,
 // between and after the products, each on a 256-byte boundary.
 struct MlpLayout {

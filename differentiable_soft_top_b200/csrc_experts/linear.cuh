@@ -872,7 +872,8 @@ cudaError_t launch_rows(const char* name, const CUtensorMap& mf, const void* x, 
   auto bound = [&](int tok, int feat) {
     return (std::min<int64_t>(a.experts + 1, a.rows) + a.rows / tok) * ((a.feat + feat - 1) / feat);
   };
-  if (e == cudaSuccess) e = map_rows(&full, x, a.depth, a.rows, x_stride, mean <= 32 ? 32 : 128);
+  full = mt;  // few rows: a full tile is one small box
+  if (e == cudaSuccess && mean > 32) e = map_rows(&full, x, a.depth, a.rows, x_stride, 128);
   if (e != cudaSuccess) return e;
   if (mean <= 32) {
     const int64_t tiles = bound(32, Shape<kMode, 32, kGated>::kTileFeat);

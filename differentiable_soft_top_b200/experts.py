@@ -80,6 +80,7 @@ def _load():
                 "linear_act_bwd": [P, i32, i64, i64, i64, P, i64, i32, P, i32, P, i64, P, P, sz, P],
                 "linear_dx": [P, i32, i64, i64, i64, P, i32, i64, P, P, i64, P, P],
                 "linear_dweight": [P, i32, i64, i64, i64, P, i64, i64, i32, P, P, P, P],
+                "linear_bwd": [P, i32, i64, i64, i64, P, P, i64, i64, P, i32, P, i32, P, P, P, P, P, sz, P],
                 "mlp_fwd": [P, i32, i64, i64, i64, P, P, i32, P, P, i32, i64, i32, P, P, i64, P, i64, P, i64, P, P, sz, P],
                 "trace_collect": [ctypes.c_char_p, sz],
             }.items():
@@ -89,6 +90,8 @@ def _load():
             lib.lapsum_experts_plan_workspace_size.restype = sz
             lib.lapsum_experts_linear_act_workspace_size.argtypes = [i64, i32, i64]
             lib.lapsum_experts_linear_act_workspace_size.restype = sz
+            lib.lapsum_experts_linear_bwd_workspace_size.argtypes = [i64, i32, i64, i32, i32]
+            lib.lapsum_experts_linear_bwd_workspace_size.restype = sz
             lib.lapsum_experts_mlp_workspace_size.argtypes = [i64, i32, i32, i64, i64, i64]
             lib.lapsum_experts_mlp_workspace_size.restype = sz
             lib.lapsum_experts_last_cuda_error.argtypes = []
@@ -377,19 +380,8 @@ def _linear_fwd(x, weight, offsets, bias, act, residual, keep, status):
     return y, h
 
 
-def linear(x, weight, offsets=None, *, bias=None, activation: str | None = None, residual=None, status=None):
-    """act(W_e x_r + b_e) + residual_r for the rows offsets[e] <= r < offsets[e + 1]
-    of expert e, on the tensor cores with fp32 sums and one rounding.
-
-    x [rows, in] bf16 or fp16; weight [experts, out, in] of that type, with
-    offsets int32 [experts + 1] on the device (a Plan's) ascending from 0, or
-    [out, in] with offsets None: one matrix for all rows.  in and out are
-    multiples of 8.  bias [experts, out] (or [out]) and residual of the type.
-    activation: None, "relu", "silu", "gelu" (by erf) or "swiglu" (silu of the
-    first half of the outputs times the second: out a multiple of 16, the
-    result half as wide).  Rows from offsets[-1] on get the residual (0).
-
-    status: an int32 [1] tensor into which STATUS_* bits are or'ed (optional)."""
+def _check_linear(x, weight, offsets, bias, activation, residual, status):
+    """The activation's number, or an error that says what is wrong."""
     _cuda(x, "x", 2)
     _dtype(x, "x", half_only=True)
     dev = x.device
@@ -408,7 +400,7 @@ def linear(x, weight, offsets=None, *, bias=None, activation: str | None = None,
     if offsets is not None:
         if not 1 <= experts <= MAX_EXPERTS:
             raise ValueError(f"weight must have 1 to {MAX_EXPERTS} experts, got {experts}")
-        offsets = _index(_cuda(offsets, "offsets", 1), "offsets", dev)
+        _index(_cuda(offsets, "offsets", 1), "offsets", dev)
         if offsets.shape[0] != experts + 1:
             raise ValueError(f"offsets must hold {experts + 1} values, got {offsets.shape[0]}")
     shape = tuple(weight.shape[:-1])
@@ -424,6 +416,27 @@ def linear(x, weight, offsets=None, *, bias=None, activation: str | None = None,
                              f"{tuple(residual.shape)}")
     if status is not None and (_cuda(status, "status", None, dev).dtype != _I32 or status.numel() < 1):
         raise TypeError("status must be an int32 tensor")
+    return act
+
+
+def linear(x, weight, offsets=None, *, bias=None, activation: str | None = None, residual=None, status=None):
+    """act(W_e x_r + b_e) + residual_r for the rows offsets[e] <= r < offsets[e + 1]
+    of expert e, on the tensor cores with fp32 sums and one rounding.
+
+    x [rows, in] bf16 or fp16; weight [experts, out, in] of that type, with
+    offsets int32 [experts + 1] on the device (a Plan's) ascending from 0, or
+    [out, in] with offsets None: one matrix for all rows.  in and out are
+    multiples of 8.  bias [experts, out] (or [out]) and residual of the type.
+    activation: None, "relu", "silu", "gelu" (by erf) or "swiglu" (silu of the
+    first half of the outputs times the second: out a multiple of 16, the
+    result half as wide).  Rows from offsets[-1] on get the residual (0).
+
+    status: an int32 [1] tensor into which STATUS_* bits are or'ed (optional)."""
+    act = _check_linear(x, weight, offsets, bias, activation, residual, status)
+    n, k = weight.shape[-2:]
+    experts = 1 if offsets is None else weight.shape[0]
+    if offsets is not None:
+        offsets = offsets.contiguous()
     if _tracked(x, weight, bias, residual):
         return _function("linear").apply(x, weight, bias, residual, offsets, act, status)
     w = _dense16(weight).view(experts, n, k)
@@ -531,7 +544,7 @@ def _combine_bwd(g, y, weights, rows, slots, need_y, need_w):
 def _linear_bwd(g, x, w, offsets, h, act, need_x, need_w, need_b, status):
     """(dx, dweight, dbias) for dy = g; h the pre-activation of act != 0."""
     experts, n, k = w.shape
-    r, dev, dt, index = x.shape[0], x.device, _dtype(x, "x"), x.get_device()
+    r, dev = x.shape[0], x.device
     gb = torch.empty((experts, n), dtype=x.dtype, device=dev) if need_b else None
     gx = torch.empty((r, k), dtype=x.dtype, device=dev) if need_x else None
     gw = torch.empty((experts, n, k), dtype=x.dtype, device=dev) if need_w else None
@@ -541,20 +554,12 @@ def _linear_bwd(g, x, w, offsets, h, act, need_x, need_w, need_b, status):
                 z.zero_()
         return gx, gw, gb
     if need_x or need_w or need_b:
-        gy = gh = _rows16(g)
-        if act or need_b:
-            gh = torch.empty((r, n), dtype=x.dtype, device=dev) if act else None
-            need = int(_load().lapsum_experts_linear_act_workspace_size(r, experts, n)) if need_b else 0
-            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-            _call("linear_act_bwd", index, gy.data_ptr(), dt, r, n, _stride(gy), _ptr(h), n, experts, _ptr(offsets), act,
-                  _ptr(gh), n, _ptr(gb), _ptr(ws), need)
-            gh = gh if act else gy
-        if need_x:
-            _call("linear_dx", index, gh.data_ptr(), dt, r, n, _stride(gh), w.data_ptr(), experts, k, _ptr(offsets),
-                  gx.data_ptr(), k, _ptr(status))
-        if need_w:
-            _call("linear_dweight", index, gh.data_ptr(), dt, r, n, _stride(gh), x.data_ptr(), k, _stride(x), experts,
-                  _ptr(offsets), gw.data_ptr(), _ptr(status))
+        g = _rows16(g)
+        need = _load().lapsum_experts_linear_bwd_workspace_size(r, experts, n, act, need_b)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        _call("linear_bwd", x.get_device(), g.data_ptr(), _DTYPES[x.dtype], r, n, _stride(g), _ptr(h), x.data_ptr(), k,
+              _stride(x), w.data_ptr(), experts, _ptr(offsets), act, _ptr(gx), _ptr(gw), _ptr(gb), _ptr(status), _ptr(ws),
+              need)
     return gx, gw, gb
 
 

@@ -216,6 +216,20 @@ LAPSUM_API int lapsum_experts_linear_dweight(const void* grad_h, int dtype, int6
                                              uint32_t* status, void* stream);
 
 /*
+ * The whole backward in one call: the three steps above, grad_h in the
+ * workspace (lapsum_experts_linear_bwd_workspace_size bytes, 256-byte aligned).
+ * Any of grad_x, grad_weight and grad_bias may be NULL; preact may be NULL for
+ * LAPSUM_ACT_NONE.  grad_x, preact and grad_bias are contiguous.
+ */
+LAPSUM_API size_t lapsum_experts_linear_bwd_workspace_size(int64_t rows, int experts, int64_t out, int activation,
+                                                           int with_bias);
+LAPSUM_API int lapsum_experts_linear_bwd(const void* grad_y, int dtype, int64_t rows, int64_t out,
+                                         int64_t grad_y_stride, const void* preact, const void* x, int64_t in,
+                                         int64_t x_stride, const void* weight, int experts, const int32_t* offsets,
+                                         int activation, void* grad_x, void* grad_weight, void* grad_bias,
+                                         uint32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * The layer in one call (forward only): plan, dispatch, product with bias and
  * activation, product with bias, weighted sum with residual, each as above,
  * for x [tokens, dim] (bf16 or fp16), chosen and weights [tokens, k], w_in

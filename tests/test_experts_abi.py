@@ -155,6 +155,24 @@ def test_products_reject_bad_arguments(lib):
     ])
 
 
+def test_linear_backward_rejects_bad_arguments(lib):
+    names = "gy dtype rows out gys pre x in_ xs w experts off act gx gw gb status ws wsb stream".split()
+    good = dict(gy=at(0), dtype=2, rows=32, out=128, gys=128, pre=at(1), x=at(2), in_=64, xs=64, w=at(3), experts=4, off=at(4),
+                act=2, gx=at(5), gw=at(6), gb=at(7), status=None, ws=at(8), wsb=1 << 20, stream=None)
+    size = lib.lapsum_experts_linear_bwd_workspace_size
+    need = size(32, 4, 128, 2, 1)
+    assert need == 32 * 128 * 2 + lib.lapsum_experts_linear_act_workspace_size(32, 4, 128)
+    assert size(32, 4, 128, 0, 0) == 0 and size(0, 4, 128, 2, 1) == 0
+    refused(lib.lapsum_experts_linear_bwd, names, good, [
+        (dict(gy=None), EINVAL), (dict(pre=None), EINVAL), (dict(x=None), EINVAL), (dict(w=None), EINVAL), (dict(off=None), EINVAL),
+        (dict(gx=None, gw=None, gb=None), EINVAL), (dict(dtype=0), EINVAL), (dict(rows=0), EINVAL), (dict(in_=60), EINVAL),
+        (dict(act=5), EINVAL), (dict(act=4, out=136, gys=136), EINVAL), (dict(gys=132), EINVAL), (dict(xs=56), EINVAL),
+        (dict(gx=at(5) + 8), EINVAL), (dict(gw=at(6) + 8), EINVAL), (dict(gx=at(0)), EINVAL), (dict(gw=at(2)), EINVAL),
+        (dict(gx=at(3)), EINVAL), (dict(gb=at(6)), EINVAL), (dict(gw=at(1)), EINVAL), (dict(ws=at(5)), EINVAL),
+        (dict(ws=None), EWORKSPACE), (dict(wsb=need - 1), EWORKSPACE), (dict(ws=at(8) + 16), EWORKSPACE),
+    ])
+
+
 def test_layer_rejects_bad_arguments(lib):
     names = "x dtype tokens dim xs w chosen k wi bi experts up act wo bo dim_out res rs out os status ws wsb stream".split()
     good = dict(x=at(0), dtype=1, tokens=8, dim=64, xs=64, w=at(1), chosen=at(2), k=2, wi=at(3), bi=at(4), experts=4, up=128,
