@@ -178,6 +178,45 @@ constexpr int full_vec() {
   return 16 / (int)sizeof(typename Elem<kDtype>::T);
 }
 
+// the pack's values in fp32; 16-bit pairs are taken apart as words
+template <int kDtype, int kVec>
+__device__ __forceinline__ void unpack(const Pack<kDtype, kVec>& p, float (&f)[kVec]) {
+  if constexpr (kVec == 1 || kDtype == LAPSUM_F32) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) f[i] = Elem<kDtype>::get(p.v[i]);
+  } else {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(p.v);
+#pragma unroll
+    for (int i = 0; i < kVec / 2; ++i) {
+      if constexpr (kDtype == LAPSUM_BF16) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(w + i));
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+      }
+    }
+  }
+}
+template <int kDtype, int kVec>
+__device__ __forceinline__ Pack<kDtype, kVec> pack(const float (&f)[kVec]) {
+  Pack<kDtype, kVec> p;
+  if constexpr (kVec == 1 || kDtype == LAPSUM_F32) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) p.v[i] = Elem<kDtype>::put(f[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec / 2; ++i) {
+      if constexpr (kDtype == LAPSUM_BF16)
+        reinterpret_cast<__nv_bfloat162*>(p.v)[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      else
+        reinterpret_cast<__half2*>(p.v)[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    }
+  }
+  return p;
+}
+
 template <int kDtype, int kVec>
 __device__ __forceinline__ Pack<kDtype, kVec> zero_pack() {
   Pack<kDtype, kVec> p;
@@ -228,7 +267,7 @@ __global__ void __launch_bounds__(kRowThreads) k_dispatch(const typename Elem<kD
 // token, which came back for 512 bytes of each row at a time, took 1.3 to 2
 // times as long).  The next token's row numbers are read ahead.
 template <int kDtype, int kVec, int kRows, int kPacks>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, 2)
     k_combine(const typename Elem<kDtype>::T* __restrict__ y, int64_t y_stride, const float* __restrict__ weights,
               const int32_t* __restrict__ rows, int64_t tokens, int k, int64_t all_rows,
               const typename Elem<kDtype>::T* __restrict__ residual, int64_t res_stride,
@@ -239,62 +278,56 @@ __global__ void __launch_bounds__(kRowThreads)
   const int in_block = kRowThreads / per_row;
   const int64_t step = (int64_t)gridDim.x * in_block;
   int64_t t = (int64_t)blockIdx.x * in_block + threadIdx.x / per_row;
-  auto look = [&](int64_t tok, int j0, int (&r)[kRows], float (&c)[kRows]) {
+  auto look = [&](int64_t tok, int j0, int (&r)[kRows]) {
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const int64_t at = tok * k + min(j0 + j, k - 1);
-      r[j] = __ldg(rows + at);
-      c[j] = weights ? __ldg(weights + at) : 1.0f;
-    }
+    for (int j = 0; j < kRows; ++j) r[j] = __ldg(rows + tok * k + min(j0 + j, k - 1));
   };
   int r[kRows], r1[kRows];
-  float c[kRows], c1[kRows];
-  if (t < tokens) look(t, 0, r1, c1);
+  if (t < tokens) look(t, 0, r1);
   for (; t < tokens; t += step) {
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      r[j] = r1[j];
-      c[j] = c1[j];
-    }
-    if (t + step < tokens) look(t + step, 0, r1, c1);
+    for (int j = 0; j < kRows; ++j) r[j] = r1[j];
+    if (t + step < tokens) look(t + step, 0, r1);
     for (int p = threadIdx.x % per_row; p < packs; p += per_row * kPacks) {
       float acc[kPacks][kVec];
 #pragma unroll
       for (int q = 0; q < kPacks; ++q) {
         P v = zero_pack<kDtype, kVec>();
         if (residual) v = reinterpret_cast<const P*>(residual + t * res_stride)[min(p + q * per_row, packs - 1)];
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) acc[q][i] = Elem<kDtype>::get(v.v[i]);
+        unpack<kDtype, kVec>(v, acc[q]);
       }
       for (int j0 = 0; j0 < k; j0 += kRows) {
-        if (k > kRows) look(t, j0, r, c);
+        if (k > kRows) look(t, j0, r);
+        // all loads first, without a branch between them (places behind the last
+        // repeat it and are not added)
         P v[kRows][kPacks];
+        float c[kRows];
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+          const P* src = reinterpret_cast<const P*>(y + ((uint64_t)(int64_t)r[j] < (uint64_t)all_rows ? (int64_t)r[j] : 0) * y_stride);
+#pragma unroll
+          for (int q = 0; q < kPacks; ++q) v[j][q] = src[min(p + q * per_row, packs - 1)];
+        }
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) c[j] = weights ? __ldg(weights + t * k + min(j0 + j, k - 1)) : 1.0f;
 #pragma unroll
         for (int j = 0; j < kRows; ++j)
           if (j0 + j < k) {
             const bool some = (uint64_t)(int64_t)r[j] < (uint64_t)all_rows;
-            const P* src = reinterpret_cast<const P*>(y + (some ? (int64_t)r[j] : 0) * y_stride);
 #pragma unroll
-            for (int q = 0; q < kPacks; ++q) v[j][q] = src[min(p + q * per_row, packs - 1)];
-          }
+            for (int q = 0; q < kPacks; ++q) {
+              if (!some) v[j][q] = zero_pack<kDtype, kVec>();  // a row that is not there adds w * 0
+              float f[kVec];
+              unpack<kDtype, kVec>(v[j][q], f);
 #pragma unroll
-        for (int j = 0; j < kRows; ++j)
-          if (j0 + j < k) {
-            const bool some = (uint64_t)(int64_t)r[j] < (uint64_t)all_rows;
-#pragma unroll
-            for (int q = 0; q < kPacks; ++q)
-#pragma unroll
-              for (int i = 0; i < kVec; ++i)  // a row that is not there adds w * 0
-                acc[q][i] = fmaf(c[j], some ? Elem<kDtype>::get(v[j][q].v[i]) : 0.0f, acc[q][i]);
+              for (int i = 0; i < kVec; ++i) acc[q][i] = fmaf(c[j], f[i], acc[q][i]);
+            }
           }
       }
 #pragma unroll
       for (int q = 0; q < kPacks; ++q)
         if (p + q * per_row < packs) {
-          P v;
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) v.v[i] = Elem<kDtype>::put(acc[q][i]);
-          reinterpret_cast<P*>(out + t * out_stride)[p + q * per_row] = v;
+          reinterpret_cast<P*>(out + t * out_stride)[p + q * per_row] = pack<kDtype, kVec>(acc[q]);
         }
     }
   }
@@ -333,14 +366,17 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (p + 32 * i < packs) {
-            P o;
+            float f[kVec];
+            unpack<kDtype, kVec>(a[i], f);
+            if (gw) {
+              float h[kVec];
+              unpack<kDtype, kVec>(b[i], h);
 #pragma unroll
-            for (int q = 0; q < kVec; ++q) {
-              const float v = Elem<kDtype>::get(a[i].v[q]);
-              if (gw) dot = fmaf(v, Elem<kDtype>::get(b[i].v[q]), dot);
-              o.v[q] = Elem<kDtype>::put(wt * v);
+              for (int q = 0; q < kVec; ++q) dot = fmaf(f[q], h[q], dot);
             }
-            if (gy) op[p + 32 * i] = o;
+#pragma unroll
+            for (int q = 0; q < kVec; ++q) f[q] *= wt;
+            if (gy) op[p + 32 * i] = pack<kDtype, kVec>(f);
           }
       }
     }
