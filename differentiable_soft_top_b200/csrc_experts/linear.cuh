@@ -438,8 +438,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
   unsigned char* tail = staging + S::kStaging;
   uint64_t* full = reinterpret_cast<uint64_t*>(tail);
   uint64_t* empty = full + kStages;
-  uint64_t* peer_full = empty + kStages;  // kPair, first block: the second's stage has landed
-  uint64_t* acc_full = peer_full + kStages;  // [2]
+  uint64_t* acc_full = empty + kStages;      // [2]
   uint64_t* acc_empty = acc_full + 2;        // [2]
   uint64_t* drained = acc_empty + 2;
   uint64_t* landed = drained + 1;            // kGradW [kStages]: copies of a ragged end
@@ -455,9 +454,8 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
     prefetch_map(&map_f);
     prefetch_map(&map_t);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full + s, 1);
+      mbar_init(full + s, kPair ? 2 : 1);  // kPair: of the first block, for both blocks' copies
       mbar_init(empty + s, 1);
-      mbar_init(peer_full + s, 1);
       mbar_init(landed + s, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -526,30 +524,33 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
           const int d = c * kDepth;
           // a ragged end is full when the zeroing warp says so
           const bool end = kMode == kGradW && t.n - d < kDepth;
-          uint64_t* bar = end ? landed + s : full + s;
           if (kMode == kGradW) {
             ends = end ? ends | 1u << s : ends & ~(1u << s);
             if (end) phases ^= 1u << s;
           }
-          mbar_arrive_expect_tx(bar, bytes);
+          const uint32_t bar = end ? smem_u32(landed + s) : kPair ? in_block(full + s, 0) : smem_u32(full + s);
+          if (kPair && !end)
+            arrive_expect_at(bar, bytes);
+          else
+            mbar_arrive_expect_tx(end ? landed + s : full + s, bytes);
           if (kMode == kForward) {
             if (kGated)
-              tma_load_5d(sa, &map_f, d, 0, 0, t.f0 / 8, t.expert, bar);
+              tma_load_5d<kPair>(sa, &map_f, d, 0, 0, t.f0 / 8, t.expert, bar);
             else
-              tma_load_3d(sa, &map_f, d, t.f0, t.expert, bar);
+              tma_load_3d<kPair>(sa, &map_f, d, t.f0, t.expert, bar);
           } else if (kMode == kGradX) {
-            tma_load_3d(sa, &map_f, t.f0, d, t.expert, bar);
-            tma_load_3d(sa + 8192, &map_f, t.f0 + 64, d, t.expert, bar);
+            tma_load_3d<kPair>(sa, &map_f, t.f0, d, t.expert, bar);
+            tma_load_3d<kPair>(sa + 8192, &map_f, t.f0 + 64, d, t.expert, bar);
           } else {
-            tma_load_2d(sa, &map_f, t.f0, t.row0 + d, bar);
-            tma_load_2d(sa + 8192, &map_f, t.f0 + 64, t.row0 + d, bar);
+            tma_load_2d<kPair>(sa, &map_f, t.f0, t.row0 + d, bar);
+            tma_load_2d<kPair>(sa + 8192, &map_f, t.f0 + 64, t.row0 + d, bar);
           }
-          if (whole) tma_load_2d(sb, &map_full, d, t.row0 + n0, bar);
+          if (whole) tma_load_2d<kPair>(sb, &map_full, d, t.row0 + n0, bar);
           for (int b = whole ? boxes : 0; b < boxes; ++b) {
             if (kMode == kGradW)
-              tma_load_2d(sb + b * kBoxBytes, &map_t, t.c0 + n0 + kBox * b, t.row0 + d, bar);
+              tma_load_2d<kPair>(sb + b * kBoxBytes, &map_t, t.c0 + n0 + kBox * b, t.row0 + d, bar);
             else
-              tma_load_2d(sb + b * kBoxBytes, &map_t, d, t.row0 + n0 + kBox * b, bar);
+              tma_load_2d<kPair>(sb + b * kBoxBytes, &map_t, d, t.row0 + n0 + kBox * b, bar);
           }
           if (used < kStages) ++used;
           if (++s == kStages) {
@@ -558,9 +559,13 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
           }
         }
       }
-      // before the block ends, its copies in flight land (bounded); after a
-      // normal end warp 1 has waited for every one of them
-      if (!ok) {
+      // Before the block ends, its copies in flight land (bounded); after a normal
+      // end warp 1 of this block, or of the pair's first, has waited for every one
+      // of them.  In a pair that ends early the first block looks after both: it
+      // arrives in place of what it would have copied to the stages that the
+      // second may have filled ahead of it, and waits for all stages.
+      if (!ok && (!kPair || half == 0)) {
+        const uint32_t s1 = s, ph1 = ph;
         for (; used; --used) {
           if (s == 0) ph ^= 1u;
           s = s == 0 ? kStages - 1 : s - 1;
@@ -569,11 +574,20 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
           else
             mbar_wait_bounded(full + s, ph, kPolls);
         }
+        s = s1, ph = ph1;
+        for (int i = 0; kPair && i < kStages; ++i) {
+          mbar_arrive(full + s);
+          mbar_wait_bounded(full + s, ph, kPolls);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
       }
     }
   } else if (warp == 1) {
-    // One lane issues and, in the second block of a pair, reports its stages.
-    if (lane == 0) {
+    // One lane issues, in a pair that of the first block.
+    if (lane == 0 && half == 0) {
       uint32_t s = 0, ph = 0, done = 0;
       bool ok = true;
       int tile = first;
@@ -585,7 +599,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
         width(cur, n, n0, own);
         if (c0 < c1) {
           const uint32_t buf = S::kSplit ? 0u : done & 1u;
-          if (half == 0) ok = wait_for(acc_empty + buf, ((S::kSplit ? done : done >> 1) & 1u) ^ 1u, gave_up);
+          ok = wait_for(acc_empty + buf, ((S::kSplit ? done : done >> 1) & 1u) ^ 1u, gave_up);
           tc_fence_after();
           const uint32_t acc = tmem + buf * kTok;
           const uint32_t idesc = instr_desc(std::is_same<T, __nv_bfloat16>::value, kMode != kForward, kMode == kGradW,
@@ -594,31 +608,19 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
             ok = wait_for(full + s, ph, gave_up);
             if (!ok) break;
             const int left = kMode == kGradW ? cur.n - c * kDepth : kDepth;
-            const bool ragged = left < kDepth;
-            if (half != 0) {
-              if (ragged)
-                arrive_at<true>(peer_full + s, 0);  // with the zeroed lines
-              else
-                arrive_at<false>(peer_full + s, 0);
-            } else {
-              if (kPair) {
-                ok = wait_for(peer_full + s, ph, gave_up);
-                if (ok && ragged) mbar_try_wait_cluster(peer_full + s, ph);  // done already: acquires
-              }
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t sa = smem_u32(ring) + s * S::kStage;
-              const uint64_t da = operand_desc(sa, kMode == kForward ? 16u : 8192u);
-              const uint64_t db = operand_desc(sa + S::kABytes, kMode == kGradW ? 8192u : 16u);
-              constexpr uint32_t kStepA = (kMode == kForward ? 32 : 2048) >> 4,
-                                 kStepB = (kMode == kGradW ? 2048 : 32) >> 4;
+            if (kPair && left < kDepth) mbar_try_wait_cluster(full + s, ph);  // done already: acquires the zeroed lines
+            tc_fence_after();
+            const uint32_t sa = smem_u32(ring) + s * S::kStage;
+            const uint64_t da = operand_desc(sa, kMode == kForward ? 16u : 8192u);
+            const uint64_t db = operand_desc(sa + S::kABytes, kMode == kGradW ? 8192u : 16u);
+            constexpr uint32_t kStepA = (kMode == kForward ? 32 : 2048) >> 4,
+                               kStepB = (kMode == kGradW ? 2048 : 32) >> 4;
 #pragma unroll
-              for (uint32_t k = 0; k < kDepth / 16; ++k)
-                if (kMode != kGradW || (int)(16 * k) < left)
-                  mma_f16<kPair>(acc, da + k * kStepA, db + k * kStepB, idesc, c != c0 || k != 0);
-              mma_commit<kPair>(empty + s);
-              if (c + 1 == c1) mma_commit<kPair>(acc_full + buf);
-            }
+            for (uint32_t k = 0; k < kDepth / 16; ++k)
+              if (kMode != kGradW || (int)(16 * k) < left)
+                mma_f16<kPair>(acc, da + k * kStepA, db + k * kStepB, idesc, c != c0 || k != 0);
+            mma_commit<kPair>(empty + s);
+            if (c + 1 == c1) mma_commit<kPair>(acc_full + buf);
             if (++s == kStages) {
               s = 0;
               ph ^= 1u;
@@ -629,7 +631,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
         // the next tile is found while this one's products run
         if (tile < tiles - step) t = tile_of<kMode, kTok, kGated>(a, table, tile + step, half);
       }
-      if (!ok && half == 0) {  // the products in flight end before their tensor memory is freed
+      if (!ok) {  // the products in flight end before their tensor memory is freed
         mma_commit<kPair>(drained);
         mbar_wait_bounded(drained, 0u, kPolls);
       }
@@ -658,7 +660,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full + s);
+      if (lane == 0) arrive_at<true>(in_block(full + s, 0));
     }
   } else if (!S::kSplit) {
     // Two warps share a quarter of the lanes and take every other 32 columns.
@@ -687,7 +689,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (kPair) arrive_at<false>(acc_empty + buf, 0);
+          if (kPair) arrive_at<false>(in_block(acc_empty + buf, 0));
           else mbar_arrive(acc_empty + buf);
         }
       };

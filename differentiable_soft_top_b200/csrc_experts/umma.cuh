@@ -10,27 +10,36 @@
 namespace lapsum {
 
 // ---- tiled copies (one box of a tensor map into shared memory) --------------
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(mbar))
-      : "memory");
+// bar: shared-window address of the barrier that gets the bytes; kPair: the one
+// of the pair's first block.
+#define LAPSUM_TMA_LOAD(dims, coords, ...)                                                                          \
+  do {                                                                                                              \
+    if (kPair)                                                                                                      \
+      asm volatile("cp.async.bulk.tensor." dims                                                                     \
+                   ".shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, " coords      \
+                   "], [%2];" ::"r"(smem_u32(dst)),                                                                 \
+                   "l"(map), "r"(bar), __VA_ARGS__                                                                  \
+                   : "memory");                                                                                     \
+    else                                                                                                            \
+      asm volatile("cp.async.bulk.tensor." dims                                                                     \
+                   ".shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, " coords "], [%2];" ::"r"( \
+                       smem_u32(dst)),                                                                              \
+                   "l"(map), "r"(bar), __VA_ARGS__                                                                  \
+                   : "memory");                                                                                     \
+  } while (0)
+
+template <bool kPair>
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  LAPSUM_TMA_LOAD("2d", "{%3, %4}", "r"(x), "r"(y));
 }
+template <bool kPair>
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  LAPSUM_TMA_LOAD("3d", "{%3, %4, %5}", "r"(x), "r"(y), "r"(z));
+}
+template <bool kPair>
 __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int x, int y, int z, int u, int v,
-                                            uint64_t* mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
-      "%6}], [%7];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(smem_u32(mbar))
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-      "[%5];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(mbar))
-      : "memory");
+                                            uint32_t bar) {
+  LAPSUM_TMA_LOAD("5d", "{%3, %4, %5, %6, %7}", "r"(x), "r"(y), "r"(z), "r"(u), "r"(v));
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -188,17 +197,25 @@ __device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t rank, floa
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(v) : "memory");
 }
 
-// One arrival at the barrier in the same place of block `rank`.  kRelease orders
-// this thread's ordinary writes before it; copies that have landed and reads of
-// tensor memory need no such order, and it is far from free.
-template <bool kRelease>
-__device__ __forceinline__ void arrive_at(uint64_t* mbar, uint32_t rank) {
+// the shared-window address of this block's `p` in block `rank`
+__device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank) {
   uint32_t there;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(smem_u32(mbar)), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(smem_u32(p)), "r"(rank));
+  return there;
+}
+// One arrival at a barrier of the cluster.  kRelease orders this thread's
+// ordinary writes before it; copies and reads of tensor memory need no such
+// order, and it is far from free.
+template <bool kRelease>
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
   if (kRelease)
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(there) : "memory");
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
   else
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(there) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_expect_at(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
 }
 // its counterpart, a poll after which what the other block's releasing arrival
 // ordered is visible
