@@ -56,7 +56,7 @@ enum Mode { kForward, kGradX, kGradW };
 constexpr int kDepth = 64;              // contraction per stage: one 128-byte line
 constexpr int kLanes = 128;             // accumulator lanes of a block
 constexpr int kTokBox = 32;             // tokens per copied box of a ragged tile (a full one: one box)
-constexpr uint32_t kPolls = 1u << 22;   // polls of a bounded wait, about a second
+constexpr uint32_t kPolls = 1u << 20;   // polls of a bounded wait, about a second
 constexpr int kGroup = 16;              // token tiles that share their features' tiles in time
 constexpr int kPitch = 80;              // bytes between staged rows of 64: conflict-free
 
@@ -862,33 +862,38 @@ cudaError_t launch(const char* name, const CUtensorMap& mf, const CUtensorMap& m
 }
 
 // Forward and input gradient: the form by the mean number of rows of an expert
-// that can have any.
+// that can have any, and by whether pairs would fill the GPU.  Measured (us,
+// forward, 64 experts, 2048 -> 2048): 24 rows few 102, many 96; 64 rows some 100,
+// many 98 (input gradient 107, 96); 128 rows some 104, many 108 (102, 112).  One
+// matrix, few pairs: 40 rows 4096 -> 4096 many 31, few 23; 100 rows some 38, few
+// 31; 512 rows 2048 -> 2048 many 24, some 21.
 template <typename T, int kMode, bool kGated>
 cudaError_t launch_rows(const char* name, const CUtensorMap& mf, const void* x, int64_t x_stride, const Args& a, int sms,
                         cudaStream_t st) {
-  CUtensorMap mt, full;
-  cudaError_t e = map_rows(&mt, x, a.depth, a.rows, x_stride, kTokBox);
   const int64_t live = std::min<int64_t>(a.experts, a.rows);
   const int64_t mean = a.rows / std::max<int64_t>(1, live);
   // tiles: at most one ragged one per expert, and one behind the last
   auto bound = [&](int tok, int feat) {
     return (std::min<int64_t>(a.experts + 1, a.rows) + a.rows / tok) * ((a.feat + feat - 1) / feat);
   };
-  full = mt;  // few rows: a full tile is one small box
-  if (e == cudaSuccess && mean > 32) e = map_rows(&full, x, a.depth, a.rows, x_stride, 128);
+  const int64_t pairs = bound(256, Shape<kMode, 256, kGated>::kTileFeat);
+  CUtensorMap mt, full;
+  cudaError_t e = map_rows(&mt, x, a.depth, a.rows, x_stride, kTokBox);
   if (e != cudaSuccess) return e;
-  if (mean <= 32) {
+  if (mean <= 16 || (mean <= 128 && 2 * pairs <= sms)) {
     const int64_t tiles = bound(32, Shape<kMode, 32, kGated>::kTileFeat);
     const int chunks = (a.depth + kDepth - 1) / kDepth;
     int ranks = 1;
     while (ranks < 8 && tiles * ranks * 2 <= 2 * sms && chunks >= 8 * ranks) ranks *= 2;
-    return launch<T, kMode, 32, kGated>(name, mf, mt, full, a, tiles * ranks, ranks, 0, st);
+    static_assert(kTokBox == 32, "a full tile is one small box");
+    return launch<T, kMode, 32, kGated>(name, mf, mt, mt, a, tiles * ranks, ranks, 0, st);
   }
-  if (mean <= 128)
+  e = map_rows(&full, x, a.depth, a.rows, x_stride, 128);  // the tokens of a full tile, of one block
+  if (e != cudaSuccess) return e;
+  if (mean > 64 && (mean <= 128 || 4 * pairs <= sms))
     return launch<T, kMode, 128, kGated>(
         name, mf, mt, full, a, std::min<int64_t>(bound(128, Shape<kMode, 128, kGated>::kTileFeat), sms), 1, 0, st);
-  return launch<T, kMode, 256, kGated>(
-      name, mf, mt, full, a, 2 * std::min<int64_t>(bound(256, Shape<kMode, 256, kGated>::kTileFeat), sms / 2), 2, 0, st);
+  return launch<T, kMode, 256, kGated>(name, mf, mt, full, a, 2 * std::min<int64_t>(pairs, sms / 2), 2, 0, st);
 }
 
 Args base_args(const Product& p) {
