@@ -73,6 +73,8 @@ struct Product {
   void* preact;
   int64_t preact_stride;
   uint32_t* status;
+  uint32_t polls;              // of a bounded device wait
+  int starve;                  // test knob: copy nothing
 };
 // kernel attributes, once per device
 cudaError_t exchange_init();

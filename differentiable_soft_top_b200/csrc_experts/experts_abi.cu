@@ -66,6 +66,15 @@ bool known(int dtype) { return dtype == LAPSUM_F32 || dtype == LAPSUM_BF16 || dt
 int size_of(int dtype) { return dtype == LAPSUM_F32 ? 4 : 2; }
 constexpr int64_t kMaxIndex = INT32_MAX;
 
+// polls of a product's bounded waits (2^20: about a second), and the test knob
+constexpr uint32_t kPolls = 1u << 20;
+std::atomic<uint32_t> g_test_polls{0};
+void set_limits(Product& p) {
+  const uint32_t test = g_test_polls.load(std::memory_order_relaxed);
+  p.polls = test ? test : kPolls;
+  p.starve = test != 0;
+}
+
 // A 16-bit matrix that tiled copies and 16-byte accesses reach: 16-byte rows.
 bool matrix16(const void* p, int64_t cols, int64_t stride) {
   return p && aligned(p, 16) && stride >= cols && stride % 8 == 0 && stride < (int64_t(1) << 37);
@@ -92,6 +101,8 @@ using namespace lapsum;
 extern "C" {
 
 const char* lapsum_experts_last_cuda_error(void) { return t_error; }
+
+void lapsum_experts_test_timeout(uint32_t polls) { g_test_polls.store(polls); }
 
 static int route_args(const void* scores, int dtype, int64_t tokens, int experts, int64_t row_stride, int k, int score,
                       const float* bias, float scale) {
@@ -285,6 +296,7 @@ int lapsum_experts_linear_fwd(const void* x, int dtype, int64_t rows, int64_t in
   p.preact = preact;
   p.preact_stride = preact_stride;
   p.status = status;
+  set_limits(p);
   return done((dtype == LAPSUM_BF16 ? launch_linear_fwd_bf16 : launch_linear_fwd_f16)(p, sms, (cudaStream_t)stream));
 }
 
@@ -354,6 +366,7 @@ int lapsum_experts_linear_dx(const void* grad_h, int dtype, int64_t rows, int64_
   p.y = grad_x;
   p.y_stride = grad_x_stride;
   p.status = status;
+  set_limits(p);
   return done((dtype == LAPSUM_BF16 ? launch_linear_dx_bf16 : launch_linear_dx_f16)(p, sms, (cudaStream_t)stream));
 }
 
@@ -384,6 +397,7 @@ int lapsum_experts_linear_dweight(const void* grad_h, int dtype, int64_t rows, i
   p.grad_h_stride = grad_h_stride;
   p.y = grad_weight;
   p.status = status;
+  set_limits(p);
   return done((dtype == LAPSUM_BF16 ? launch_linear_dweight_bf16 : launch_linear_dweight_f16)(p, sms, (cudaStream_t)stream));
 }
 

@@ -56,7 +56,6 @@ enum Mode { kForward, kGradX, kGradW };
 constexpr int kDepth = 64;              // contraction per stage: one 128-byte line
 constexpr int kLanes = 128;             // accumulator lanes of a block
 constexpr int kTokBox = 32;             // tokens per copied box of a ragged tile (a full one: one box)
-constexpr uint32_t kPolls = 1u << 20;   // polls of a bounded wait, about a second
 constexpr int kGroup = 16;              // token tiles that share their features' tiles in time
 constexpr int kPitch = 80;              // bytes between staged rows of 64: conflict-free
 
@@ -75,6 +74,8 @@ struct Args {
   void* preact;
   int64_t preact_stride;
   uint32_t* status;
+  uint32_t polls;    // of a bounded wait before it gives up
+  int starve;        // test knob: nothing is copied, so that waits run out
 };
 
 template <int kMode, int kTok, bool kGated>
@@ -216,17 +217,17 @@ __device__ __forceinline__ Tile tile_of(const Args& a, const int* table, int til
 }
 
 // ---- bounded waits: a block that has given up somewhere gives up everywhere --------------
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile uint32_t* gave_up) {
-  for (uint32_t i = 0; i < kPolls; ++i) {
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile uint32_t* gave_up, uint32_t polls) {
+  for (uint32_t i = 0; i < polls; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 63u) == 63u && *gave_up) return false;
   }
   *gave_up = 1u;
   return false;
 }
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile uint32_t* gave_up) {
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile uint32_t* gave_up, uint32_t polls) {
   if (mbar_try_wait(bar, parity)) return true;
-  return wait_slow(bar, parity, gave_up);
+  return wait_slow(bar, parity, gave_up, polls);
 }
 
 // ---- epilogue: a warp's 32 accumulator lanes x 32 columns --------------------------------
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
         const int boxes = (own + kBox - 1) / kBox;
         const uint32_t bytes = S::kABytes + boxes * kBoxBytes;
         for (int c = c0; c < c1; ++c) {
-          if (!wait_for(empty + s, ph ^ 1u, gave_up)) {
+          if (a.starve || !wait_for(empty + s, ph ^ 1u, gave_up, a.polls)) {
             ok = false;
             break;
           }
@@ -570,14 +571,14 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
           if (s == 0) ph ^= 1u;
           s = s == 0 ? kStages - 1 : s - 1;
           if (kMode == kGradW && (ends >> s & 1u))
-            mbar_wait_bounded(landed + s, (phases >> s & 1u) ^ 1u, kPolls);
+            mbar_wait_bounded(landed + s, (phases >> s & 1u) ^ 1u, a.polls);
           else
-            mbar_wait_bounded(full + s, ph, kPolls);
+            mbar_wait_bounded(full + s, ph, a.polls);
         }
         s = s1, ph = ph1;
         for (int i = 0; kPair && i < kStages; ++i) {
           mbar_arrive(full + s);
-          mbar_wait_bounded(full + s, ph, kPolls);
+          mbar_wait_bounded(full + s, ph, a.polls);
           if (++s == kStages) {
             s = 0;
             ph ^= 1u;
@@ -599,13 +600,13 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
         width(cur, n, n0, own);
         if (c0 < c1) {
           const uint32_t buf = S::kSplit ? 0u : done & 1u;
-          ok = wait_for(acc_empty + buf, ((S::kSplit ? done : done >> 1) & 1u) ^ 1u, gave_up);
+          ok = wait_for(acc_empty + buf, ((S::kSplit ? done : done >> 1) & 1u) ^ 1u, gave_up, a.polls);
           tc_fence_after();
           const uint32_t acc = tmem + buf * kTok;
           const uint32_t idesc = instr_desc(std::is_same<T, __nv_bfloat16>::value, kMode != kForward, kMode == kGradW,
                                             kLanes * (kPair ? 2 : 1), n);
           for (int c = c0; ok && c < c1; ++c) {
-            ok = wait_for(full + s, ph, gave_up);
+            ok = wait_for(full + s, ph, gave_up, a.polls);
             if (!ok) break;
             const int left = kMode == kGradW ? cur.n - c * kDepth : kDepth;
             if (kPair && left < kDepth) mbar_try_wait_cluster(full + s, ph);  // done already: acquires the zeroed lines
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
       }
       if (!ok) {  // the products in flight end before their tensor memory is freed
         mma_commit<kPair>(drained);
-        mbar_wait_bounded(drained, 0u, kPolls);
+        mbar_wait_bounded(drained, 0u, a.polls);
       }
     }
   } else if (kMode == kGradW && warp == 2 + S::kEpilogue) {
@@ -651,7 +652,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
       int n, n0, own;
       width(t, n, n0, own);
       const uint32_t s = (next - 1) % kStages;
-      ok = __all_sync(0xffffffffu, wait_for(landed + s, phases >> s & 1u, gave_up));
+      ok = __all_sync(0xffffffffu, wait_for(landed + s, phases >> s & 1u, gave_up, a.polls));
       phases ^= 1u << s;
       if (!ok) break;
       if ((lane >> 3) < 2 + (own + 63) / 64) {
@@ -682,7 +683,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
           get_rows<kGated>(res, a.residual, t.row0 + 32 * part, a.residual_stride, feat0, a.feat, n - 32 * part, lane);
       }
       if (sums) {
-        ok = ok && __all_sync(0xffffffffu, wait_for(acc_full + buf, (done >> 1) & 1u, gave_up));
+        ok = ok && __all_sync(0xffffffffu, wait_for(acc_full + buf, (done >> 1) & 1u, gave_up, a.polls));
         tc_fence_after();
       }
       auto release = [&] {  // this warp's columns are in registers
@@ -746,7 +747,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
         load_bias<T, kGated>(a, t, feat0, bias, lane);
         if (a.residual) get_rows<kGated>(res, a.residual, t.row0, a.residual_stride, feat0, a.feat, t.n, lane);
         if (s0 < s1) {
-          ok = __all_sync(0xffffffffu, wait_for(acc_full, 0u, gave_up));
+          ok = __all_sync(0xffffffffu, wait_for(acc_full, 0u, gave_up, a.polls));
           tc_fence_after();
         }
         if (s0 < s1 && ok) {
@@ -905,6 +906,8 @@ Args base_args(const Product& p) {
   a.y = p.y;
   a.y_stride = p.y_stride;
   a.status = p.status;
+  a.polls = p.polls;
+  a.starve = p.starve;
   return a;
 }
 

@@ -98,6 +98,8 @@ def _load():
             lib.lapsum_experts_last_cuda_error.restype = ctypes.c_char_p
             lib.lapsum_experts_launch_count.argtypes = []
             lib.lapsum_experts_launch_count.restype = ctypes.c_uint64
+            lib.lapsum_experts_test_timeout.argtypes = [ctypes.c_uint32]
+            lib.lapsum_experts_test_timeout.restype = None
             lib.lapsum_experts_trace_enable.argtypes = [i32]
             lib.lapsum_experts_trace_enable.restype = None
             _lib = lib

@@ -247,6 +247,15 @@ LAPSUM_API int lapsum_experts_mlp_fwd(const void* x, int dtype, int64_t tokens, 
                                       int64_t residual_stride, void* out, int64_t out_stride, uint32_t* status,
                                       void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Test knob, process-wide: with polls > 0 the products launched from now on
+ * copy nothing and their waits give up after that many polls, so that they end
+ * with LAPSUM_EXPERTS_TIMEOUT and NaN in every row that an expert owns (a weight
+ * gradient: in every expert that has rows).  Nothing waits forever and no fault
+ * is raised.  0: as usual again.
+ */
+LAPSUM_API void lapsum_experts_test_timeout(uint32_t polls);
+
 /* Text of the CUDA error behind the last LAPSUM_ECUDA that this library
    returned on the calling host thread. */
 LAPSUM_API const char* lapsum_experts_last_cuda_error(void);

@@ -657,3 +657,230 @@ def test_launches_are_counted_and_traced():
     assert lt.launch_count() - before == 6
     assert set(names) == {"k_route_fwd", "k_plan_place", "k_dispatch", "k_product_fwd", "k_combine"}
     assert names["k_product_fwd"][0] == 2
+
+
+# ---------------------------------------------------------------------------
+# what users do around the operators
+# ---------------------------------------------------------------------------
+def test_one_call_layer_equals_its_steps():
+    logits, x, w_in, w_out, k = small_layer(seed=101)
+    b_in, b_out = randn(12, 96, seed=1, dtype=BF16), randn(12, 64, seed=2, dtype=BF16)
+    logits[3] = -INF  # a token without experts keeps its residual
+    w, c = ex.route(logits, k)
+    p = ex.plan(c, 12)
+    h = ex.linear(ex.dispatch(x, p), w_in, p.offsets, bias=b_in, activation="swiglu")
+    y = ex.combine(ex.linear(h, w_out, p.offsets, bias=b_out), w, p, residual=x)
+    out = ex.mlp(x, w, c, w_in, w_out, b_in=b_in, b_out=b_out, residual=x)
+    assert torch.equal(out, y) and torch.equal(out[3], x[3])
+    with torch.enable_grad():
+        tracked = ex.mlp(x.detach().requires_grad_(), w, c, w_in, w_out, b_in=b_in, b_out=b_out, residual=x)
+    assert torch.equal(tracked, out)
+    # strided x and residual, a wider output buffer's neighbour left alone
+    wide = randn(96, 70, dtype=BF16)
+    wide[:, 3:67] = x
+    assert torch.equal(ex.mlp(wide[:, 3:67], w, c, w_in, w_out, b_in=b_in, b_out=b_out, residual=wide[:, 3:67]), out)
+    empty = ex.mlp(x[:0], w[:0], c[:0], w_in, w_out)
+    assert empty.shape == (0, 64)
+
+
+def test_every_subset_of_gradients():
+    """A leaf that wants no gradient changes nothing for the others."""
+    x, w, off, b, res, _ = linear_case(150, 4, 64, 128, "silu", True, True, 9, BF16, seed=111)
+    g = randn(150, 128, seed=112, dtype=BF16)
+    full = None
+    for mask in (15, 1, 2, 4, 8, 6, 9):
+        leaves = [t.detach().requires_grad_(bool(mask >> i & 1)) for i, t in enumerate((x, w, b, res))]
+        y = ex.linear(leaves[0], leaves[1], off, bias=leaves[2], activation="silu", residual=leaves[3])
+        got = torch.autograd.grad(y, [t for t in leaves if t.requires_grad], g)
+        full = full or got
+        want = [full[i] for i in range(4) if mask >> i & 1]
+        assert all(torch.equal(a, c) for a, c in zip(got, want))
+
+
+def test_expanded_gradients_and_inputs():
+    """Gradients of broadcast inputs are summed, stride-0 gradients are read as they are meant."""
+    x, w, off, _, _, _ = linear_case(60, 3, 64, 64, None, False, False, 0, BF16, seed=121)
+    row = randn(1, 64, seed=122, dtype=BF16).requires_grad_()
+    y = ex.linear(x, w, off, residual=row.expand(60, 64))
+    y.sum().backward()
+    assert torch.equal(row.grad, torch.full_like(row, 60.0))
+    p = ex.plan(some_choice(60, 2, 3, dropped=0.0), 3)
+    weights = torch.full((60, 1), 0.5, device="cuda", requires_grad=True)
+    yy = randn(120, 64, seed=123)
+    ex.combine(yy, weights.expand(60, 2), p).sum().backward()
+    want = yy[p.rows.long()].double().sum((1, 2)).view(60, 1)
+    size = yy[p.rows.long()].double().abs().sum((1, 2)).view(60, 1)
+    assert ((weights.grad.double() - want).abs() <= 130 * E32 * size).all()
+
+
+def test_differentiating_twice_is_refused():
+    x = randn(4, 8, seed=131).requires_grad_()
+    w, _ = ex.route(x, 2)
+    with pytest.raises(RuntimeError, match="twice"):
+        torch.autograd.grad(w.sum(), x, create_graph=True)
+
+
+def test_route_gradient_against_differences():
+    """Central differences of the operator itself: step h, truncation h^2 / 6 times a third derivative below 1, fp32
+    noise of a few 2^-23 over 2 h."""
+    h = 2.0 ** -6
+    for score in ("softmax", "sigmoid", "identity"):
+        for renorm in (False, True):
+            x = randn(6, 10, seed=141)
+            x = (x.sigmoid() + torch.arange(10, device="cuda") if score == "identity" else x + 0.5 * torch.arange(10, device="cuda"))
+            x.requires_grad_()
+            g = randn(6, 4, seed=142)
+            w, c = ex.route(x, 4, score=score, renormalize=renorm)
+            (dx,) = torch.autograd.grad(w, x, g)
+            for i in range(10):
+                step = torch.zeros_like(x)
+                step[:, i] = h
+                up, cu = ex.route((x + step).detach(), 4, score=score, renormalize=renorm)
+                dn, cd = ex.route((x - step).detach(), 4, score=score, renormalize=renorm)
+                same = (cu == c).all(1) & (cd == c).all(1)  # at fixed choice
+                diff = ((up - dn) * g).sum(1) / (2 * h)
+                tol = g.abs().sum(1) * (h * h / 6 + 16 * E32 * 10 / h)
+                assert ((diff - dx[:, i]).abs() <= tol)[same].all(), (score, renorm, i)
+
+
+def test_tests_own_derivatives_against_differences():
+    h = torch.linspace(-4, 4, 257, dtype=torch.float64)
+    for act in ("silu", "gelu"):
+        x = h.clone().requires_grad_()
+        (d,) = torch.autograd.grad(act64(x, act).sum(), x)
+        e = 1e-5
+        assert ((act64(h + e, act) - act64(h - e, act)) / (2 * e) - d).abs().max() < 1e-9
+
+
+def test_a_waiting_product_gives_up_and_says_so():
+    """Copies that never come (a test knob): status, NaN in the rows of experts, and the next call works."""
+    lib = ex._load()
+    for case in ((40, 4, 256, 512, None), (400, 4, 256, 512, "swiglu"), (2000, 2, 256, 512, "gelu"), (8, 0, 2048, 256, None)):
+        r, e, k, n, act = case
+        x, w, off, _, _, ends = linear_case(r, e, k, n, act, False, False, 3 if e else 0, BF16, seed=r)
+        want = ex.linear(x, w, off, activation=act)
+        w3 = w.view(-1, n, k)
+        gh, gx, gw = randn(r, n, seed=5, dtype=BF16), torch.zeros_like(x), torch.zeros_like(w)
+        grads = lambda st: (ex._call("linear_dx", 0, gh.data_ptr(), 1, r, n, n, w.data_ptr(), w3.shape[0], k,  # noqa: E731
+                                     ex._ptr(off), gx.data_ptr(), k, st.data_ptr()),
+                            ex._call("linear_dweight", 0, gh.data_ptr(), 1, r, n, n, x.data_ptr(), k, k, w3.shape[0],
+                                     ex._ptr(off), gw.data_ptr(), st.data_ptr()))
+        status, status2 = torch.zeros(2, dtype=torch.int32, device="cuda").chunk(2)
+        lib.lapsum_experts_test_timeout(500)
+        try:
+            y = ex.linear(x, w, off, activation=act, status=status)
+            grads(status2)
+            torch.cuda.synchronize()
+        finally:
+            lib.lapsum_experts_test_timeout(0)
+        assert int(status) == int(status2) == ex.STATUS_TIMEOUT
+        used = ends[-1]
+        assert y[:used].isnan().all() and (y[used:] == 0).all()
+        assert gx[:used].isnan().all() and (gx[used:] == 0).all()
+        for i in range(len(ends) - 1):
+            g = gw.view(-1, n, k)[i]
+            assert g.isnan().all() if ends[i + 1] > ends[i] else (g == 0).all()
+        status.zero_()
+        assert torch.equal(ex.linear(x, w, off, activation=act, status=status), want) and int(status) == 0
+        grads(status)
+        assert int(status) == 0 and not gx.isnan().any() and not gw.isnan().any()
+
+
+def test_offsets_out_of_range_are_never_followed():
+    """Nonsense offsets give nonsense rows, but nothing outside the arrays is touched."""
+    x, w, _, b, _, _ = linear_case(300, 5, 64, 128, "silu", True, False, 0, BF16, seed=151)
+    for bad in ([-5, 10**9, 3, 250, -2**31, 2**31 - 1], [300, 200, 100, 50, 20, 0], [7, 7, 7, 7, 7, 7], [0, 400, 400, 400, 400, 400]):
+        off = torch.tensor(bad, dtype=torch.int64).to(torch.int32).cuda()
+        leaves = [t.detach().requires_grad_() for t in (x, w, b)]
+        y = ex.linear(leaves[0], leaves[1], off, bias=leaves[2], activation="silu")
+        torch.autograd.grad(y, leaves, torch.ones_like(y))
+        torch.cuda.synchronize()
+    # and the next good call is right
+    check_linear(300, 5, 64, 128, "silu", True, False, 7, BF16, seed=151)
+
+
+def test_outputs_stay_inside_their_rows():
+    """Neighbours of a strided output, and what lies behind it, keep their values."""
+    r, n, k = 70, 40, 64
+    x, w, off, _, _, ends = linear_case(r, 3, k, n, None, False, False, 5, BF16, seed=161)
+    want = ex.linear(x, w, off)
+    buf = torch.full((r + 4, 64), 7.0, dtype=BF16, device="cuda")
+    ex._call("linear_fwd", 0, x.data_ptr(), 1, r, k, k, w.data_ptr(), 3, n, off.data_ptr(), None, 0, None, 0, buf.data_ptr(),
+             64, None, 0, None)
+    assert torch.equal(buf[:r, :n], want)
+    assert (buf[:, n:] == 7).all() and (buf[r:] == 7).all()
+    pre = torch.full((r, n), 7.0, dtype=BF16, device="cuda")
+    ex._call("linear_fwd", 0, x.data_ptr(), 1, r, k, k, w.data_ptr(), 3, n, off.data_ptr(), None, 1, None, 0, buf.data_ptr(),
+             64, pre.data_ptr(), n, None)
+    assert torch.equal(pre[:ends[-1]], want[:ends[-1]]) and (pre[ends[-1]:] == 7).all()
+
+
+@pytest.mark.slow
+def test_arrays_longer_than_32_bits_count():
+    """Rows beyond the 2^31st element of x, y and the exchanged rows."""
+    r, n = 140_000, 16_384  # 2.3e9 values
+    x, w = randn(r, 64, seed=171, dtype=BF16), randn(n, 64, seed=172, dtype=BF16)
+    y = ex.linear(x, w)
+    for s in (slice(0, 3), slice(131_070, 131_074), slice(r - 3, r)):
+        ref = x[s].double() @ w.double().T
+        size = x[s].double().abs() @ w.double().abs().T
+        assert ((y[s].double() - ref).abs() <= half_step(BF16) * ref.abs() + 66 * E32 * size).all()
+    c = torch.arange(r, device="cuda", dtype=torch.int32).remainder(7).view(r, 1)
+    p = ex.plan(c, 7)
+    rows = ex.dispatch(y, p)
+    for t in (0, 131_072, r - 1):
+        assert torch.equal(rows[int(p.rows[t, 0])], y[t])
+    back = ex.combine(rows, torch.ones(r, 1, device="cuda"), p)
+    assert torch.equal(back[-1000:], y[-1000:])
+    (gx,) = torch.autograd.grad(ex.linear(x.requires_grad_(), w), x, y)
+    ref, size = y[-4:].double() @ w.double(), y[-4:].double().abs() @ w.double().abs()
+    assert ((gx[-4:].double() - ref).abs() <= half_step(BF16) * ref.abs() + (n + 2) * E32 * size).all()
+
+
+@pytest.mark.parametrize("call,error,match", [
+    (lambda t: ex.route(t.x, 0), ValueError, "k must"),
+    (lambda t: ex.route(t.x, 65), ValueError, "k must"),
+    (lambda t: ex.route(t.x, 2, score="tanh"), ValueError, "score"),
+    (lambda t: ex.route(t.x, 2, groups=5), ValueError, "groups"),
+    (lambda t: ex.route(t.x, 2, groups=4, groups_kept=5), ValueError, "groups"),
+    (lambda t: ex.route(t.x, 2, group_top=3), ValueError, "groups"),
+    (lambda t: ex.route(t.x, 2, scale=0.0), ValueError, "scale"),
+    (lambda t: ex.route(t.x, 2, bias=t.x[0].double()), ValueError, "bias"),
+    (lambda t: ex.route(t.x.double(), 2), TypeError, "scores"),
+    (lambda t: ex.route(t.x[0], 2), ValueError, "2-D"),
+    (lambda t: ex.plan(t.c.long(), 4), TypeError, "int32"),
+    (lambda t: ex.plan(t.c, 0), ValueError, "experts"),
+    (lambda t: ex.plan(t.c.repeat(1, 20), 4), ValueError, "places"),
+    (lambda t: ex.dispatch(t.x[:5], t.p), ValueError, "tokens"),
+    (lambda t: ex.combine(t.x, t.w, t.p), ValueError, "rows"),
+    (lambda t: ex.combine(t.rows, t.w.half(), t.p), ValueError, "weights"),
+    (lambda t: ex.combine(t.rows, t.w, t.p, residual=t.x.half()), ValueError, "residual"),
+    (lambda t: ex.linear(t.x, t.m[0]), TypeError, "bfloat16"),
+    (lambda t: ex.linear(t.h, t.m[0].half()), TypeError, "weight"),
+    (lambda t: ex.linear(t.h, t.m), ValueError, "2-D"),
+    (lambda t: ex.linear(t.h, t.m, t.off[:3]), ValueError, "offsets"),
+    (lambda t: ex.linear(t.h, t.m, t.off.long()), TypeError, "int32"),
+    (lambda t: ex.linear(t.h, t.m[:, :20], t.off), ValueError, "multiples"),
+    (lambda t: ex.linear(t.h[:, :60], t.m[..., :60], t.off), ValueError, "multiples"),
+    (lambda t: ex.linear(t.h, t.m[:, :24], t.off, activation="swiglu"), ValueError, "multiples"),
+    (lambda t: ex.linear(t.h, t.m, t.off, activation="tanh"), ValueError, "activation"),
+    (lambda t: ex.linear(t.h, t.m, t.off, bias=t.m[0, 0]), ValueError, "bias"),
+    (lambda t: ex.linear(t.h, t.m, t.off, residual=t.h[:, :8]), ValueError, "residual"),
+    (lambda t: ex.mlp(t.h, t.w, t.c, t.m, t.m[:, :, :8]), ValueError, "w_out"),
+    (lambda t: ex.mlp(t.h, t.w, t.c[:3], t.m, t.m, activation=None), ValueError, "chosen"),
+    (lambda t: ex.mlp(t.h, t.w[:, :1], t.c, t.m, t.m, activation=None), ValueError, "weights"),
+])
+def test_binding_refuses(call, error, match):
+    class T:
+        x = randn(6, 64)
+        c = torch.zeros(6, 2, dtype=torch.int32, device="cuda")
+        w = torch.ones(6, 2, device="cuda")
+        p = ex.plan(c, 4)
+        rows = randn(12, 64)
+        h = x.to(BF16)
+        m = randn(4, 64, 64, dtype=BF16)
+        off = torch.tensor([0, 2, 2, 4, 6], dtype=torch.int32, device="cuda")
+    before = lt.launch_count()
+    with pytest.raises(error, match=match):
+        call(T)
+    assert lt.launch_count() == before
