@@ -48,7 +48,7 @@ template <int N>
 __device__ __forceinline__ void differentiate(float (&g)[N], const float (&h)[N], int act) {
   if (act == LAPSUM_ACT_RELU) {
 #pragma unroll
-    for (int c = 0; c < N; ++c) g[c] = h[c] > 0.0f ? g[c] : 0.0f * g[c];
+    for (int c = 0; c < N; ++c) g[c] = h[c] <= 0.0f ? 0.0f : g[c];
   } else if (act == LAPSUM_ACT_SILU) {  // s (1 + h (1 - s))
 #pragma unroll
     for (int c = 0; c < N; ++c) {

@@ -125,15 +125,21 @@ __device__ __forceinline__ uint32_t shuffle_xor<uint32_t>(uint32_t v, int d) {
   return __shfl_xor_sync(kAll, v, d);
 }
 
+template <typename K>
+__device__ __forceinline__ typename Order<K>::O raw_base() {
+  return ordered((K)-INFINITY) - 31u;
+}
+
 // o: the ordered keys of this lane's experts (0: not there)
 template <typename K, bool kRaw, int kPer>
 __device__ __forceinline__ void keys_of(const Rule& r, const Keys& in, const float (&l)[kPer], const float (&b)[kPer],
                                         typename Order<K>::O (&o)[kPer]) {
   using O = typename Order<K>::O;
   if (kRaw) {
-    // from the key of -inf, which becomes 0, to those of finite scores
+    // counted from the key of -inf, so that the lowest finite score has 32 (what
+    // is below stands for nothing once the last 5 bits are replaced)
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = ordered((K)l[i]) - ordered((K)-INFINITY);
+    for (int i = 0; i < kPer; ++i) o[i] = l[i] == -INFINITY ? O(0) : ordered((K)l[i]) - raw_base<K>();
     return;
   }
   const K top = (K)in.top;
@@ -191,7 +197,7 @@ __device__ __forceinline__ bool keep_groups(const Rule& r, const Keys& in, const
       }
     }
   }
-  const O from = r.raw ? ordered((K)-INFINITY) : O(0);
+  const O from = r.raw ? raw_base<K>() : O(0);
   K value = first ? key_of(first + from) : (K)-INFINITY;
   if (r.top == 2 && second) value += key_of(second + from);
   if (g >= r.groups) value = -INFINITY;
@@ -599,6 +605,8 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? 8 : kPer == 16 ? 6 : 3) 
   r.raw = kRaw;
   r.lanes = r.size % kPer == 0 && ((r.size / kPer) & (r.size / kPer - 1)) == 0 ? r.size / kPer : 0;
   const bool soft = a.score == LAPSUM_SCORE_SOFTMAX && (!r.raw || !a.renormalize);
+  // the sum of softmax scores whose order is that of the scores holds the largest
+  const bool check_sum = a.score == LAPSUM_SCORE_SIGMOID || soft;
   const int64_t step = (int64_t)gridDim.x * kWarps;
   int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   float b[kPer], ahead[kPer];
@@ -647,7 +655,9 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? 8 : kPer == 16 ? 6 : 3) 
           const float top = chosen_max(v, a.k);
           const float p = mine >= 0 ? expf(v - top) : 0.0f;
           const float total = chosen_sum(p, a.k);
-          w = mine >= 0 ? a.scale * __fdividef(p, total) : 0.0f;  // 1 <= total <= k
+          // scores that vanish in fp64 too count as 0, and so does their sum
+          const bool some = (a.score == LAPSUM_SCORE_SOFTMAX && soft ? top - in.top : top) > -745.0f || !check_sum;
+          w = mine >= 0 && some ? a.scale * __fdividef(p, total) : 0.0f;  // 1 <= total <= k
         }
       } else if (a.score == LAPSUM_SCORE_SOFTMAX) {
         w = mine >= 0 ? a.scale * (expf(s - in.top) * in.scale) : 0.0f;

