@@ -24,9 +24,10 @@
 //          where a block alone would copy 48 KB, more than L2 delivers in the
 //          512 cycles of that product
 //   some   one block, 128 tokens
-//   few    one tile of 32 tokens per cluster of 1, 2, 4 or 8 blocks, which
-//          split the contraction and join their fp32 partials through
-//          distributed shared memory in the order of rank
+//   few    one block, 32 tokens, two blocks per SM; where there are fewer tiles
+//          than that, one tile per cluster of 2, 4 or 8 blocks, which split the
+//          contraction and join their fp32 partials through distributed shared
+//          memory in the order of rank
 //
 // Gated weights (silu(gate) * up) are copied interleaved, 8 rows of one and 8
 // of the other, so that a thread holds the gate and the up value of a feature.
@@ -78,18 +79,18 @@ struct Args {
   int starve;        // test knob: nothing is copied, so that waits run out
 };
 
-template <int kMode, int kTok, bool kGated>
+template <int kMode, int kTok, bool kGated, bool kSplit>
 struct Shape {
   static constexpr bool kPair = kTok == 256;
-  static constexpr bool kSplit = kTok == 32;       // few rows: clusters, two blocks per SM
-  static constexpr int kEpilogue = kSplit ? 4 : 8;  // warps: one or two per quarter of the lanes
+  static constexpr bool kFew = kTok == 32;         // two blocks per SM
+  static constexpr int kEpilogue = kFew ? 4 : 8;    // warps: one or two per quarter of the lanes
   static constexpr int kThreads = 64 + 32 * kEpilogue + (kMode == kGradW ? 32 : 0);
   static constexpr int kFeat = kLanes / (kGated ? 2 : 1);           // features of a block's tile
   static constexpr int kTileFeat = kFeat * (kPair ? 2 : 1);         // of a tile
   static constexpr int kABytes = kLanes * 128;
   static constexpr int kBBytes = (kPair ? kTok / 2 : kTok) * 128;
   static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kStages = kSplit ? 4 : 196 * 1024 / kStage;
+  static constexpr int kStages = kFew ? 4 : 196 * 1024 / kStage;
   static constexpr int kTmemCols = kSplit ? 32 : 2 * kTok;
   // (the split form stages in the ring; here its ranks' partials arrive)
   static constexpr int kStaging = kSplit ? 32 * kLanes * 4 : kEpilogue * 32 * kPitch;
@@ -177,9 +178,9 @@ __device__ __forceinline__ void build_table(const Args& a, int* table) {
   __syncthreads();
 }
 
-template <int kMode, int kTok, bool kGated>
+template <int kMode, int kTok, bool kGated, bool kSplit>
 __device__ __forceinline__ Tile tile_of(const Args& a, const int* table, int tile, int half) {
-  using S = Shape<kMode, kTok, kGated>;
+  using S = Shape<kMode, kTok, kGated, kSplit>;
   Tile t;
   const int ftiles = (a.feat + S::kTileFeat - 1) / S::kTileFeat;
   t.c0 = 0;
@@ -430,11 +431,11 @@ __device__ __forceinline__ void fill(float (&v)[2][16], float x) {
 
 // map_f: the weights (kGradW: dH); map_t: the tokens' rows in small boxes,
 // map_full: in boxes of a full tile
-template <typename T, int kMode, int kTok, bool kGated>
-__global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kMode, kTok, kGated>::kSplit ? 2 : 1)
+template <typename T, int kMode, int kTok, bool kGated, bool kSplit>
+__global__ void __launch_bounds__(Shape<kMode, kTok, kGated, kSplit>::kThreads, kTok == 32 ? 2 : 1)
     k_product(const __grid_constant__ CUtensorMap map_f, const __grid_constant__ CUtensorMap map_t,
               const __grid_constant__ CUtensorMap map_full, const Args a, int tiles_grad_w) {
-  using S = Shape<kMode, kTok, kGated>;
+  using S = Shape<kMode, kTok, kGated, kSplit>;
   constexpr int kStages = S::kStages;
   constexpr bool kPair = S::kPair;
   extern __shared__ unsigned char smem_raw[];
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
   int* table = reinterpret_cast<int*>(tail + 512);
 
   grid_launch_next();
-  if (S::kSplit) cluster_arrive();  // waited for before the first access to another block's memory
+  if (kSplit) cluster_arrive();  // waited for before the first access to another block's memory
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = kPair ? (int)cluster_rank() : 0;
   if (threadIdx.x == 0) {
@@ -482,14 +483,14 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
 
   const int ftiles = (a.feat + S::kTileFeat - 1) / S::kTileFeat;
   const int tiles = kMode == kGradW ? tiles_grad_w : table[a.experts + 1] * ftiles;
-  const int ranks = S::kSplit ? (int)cluster_size() : kPair ? 2 : 1;
-  const int rank = S::kSplit ? (int)cluster_rank() : 0;
+  const int ranks = kSplit ? (int)cluster_size() : kPair ? 2 : 1;
+  const int rank = kSplit ? (int)cluster_rank() : 0;
   // few rows: the grid holds a cluster for every tile there can be
-  const int first = (int)blockIdx.x / ranks, step = S::kSplit ? max(tiles, 1) : (int)gridDim.x / ranks;
+  const int first = (int)blockIdx.x / ranks, step = kSplit ? max(tiles, 1) : (int)gridDim.x / ranks;
 
   // kSplit: this block's share of a tile's contraction
   auto share = [&](const Tile& t, int& c0, int& c1) {
-    if (!S::kSplit) {
+    if (!kSplit) {
       c0 = 0;
       c1 = t.chunks;
       return;
@@ -512,14 +513,14 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
       uint32_t ends = 0, phases = 0;     // kGradW, a bit per stage: holds a ragged end; its barrier's phase
       bool ok = true;
       for (int tile = first; ok && tile < tiles; tile += step) {
-        const Tile t = tile_of<kMode, kTok, kGated>(a, table, tile, half);
+        const Tile t = tile_of<kMode, kTok, kGated, kSplit>(a, table, tile, half);
         int c0, c1, n, n0, own;
         share(t, c0, c1);
         width(t, n, n0, own);
         constexpr int kBox = kMode == kGradW ? 64 : kTokBox, kBoxBytes = kMode == kGradW ? 8192 : kTokBox * 128;
         // more than two small boxes: one of the full height (rows beyond the tile's
         // are copied in vain; what limits is the number of copies)
-        const bool whole = kMode != kGradW && !S::kSplit && own > 2 * kTokBox;
+        const bool whole = kMode != kGradW && !S::kFew && own > 2 * kTokBox;
         const int boxes = (own + kBox - 1) / kBox;
         const uint32_t bytes = S::kABytes + (whole ? S::kBBytes : boxes * kBoxBytes);
         for (int c = c0; c < c1; ++c) {
@@ -599,15 +600,15 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
       uint32_t s = 0, ph = 0, done = 0;
       bool ok = true;
       int tile = first;
-      Tile t = tile_of<kMode, kTok, kGated>(a, table, min(tile, max(tiles - 1, 0)), half);
+      Tile t = tile_of<kMode, kTok, kGated, kSplit>(a, table, min(tile, max(tiles - 1, 0)), half);
       for (; ok && tile < tiles; tile += step) {
         const Tile cur = t;
         int c0, c1, n, n0, own;
         share(cur, c0, c1);
         width(cur, n, n0, own);
         if (c0 < c1) {
-          const uint32_t buf = S::kSplit ? 0u : done & 1u;
-          ok = wait_for(acc_empty + buf, ((S::kSplit ? done : done >> 1) & 1u) ^ 1u, gave_up, a.polls);
+          const uint32_t buf = kSplit ? 0u : done & 1u;
+          ok = wait_for(acc_empty + buf, ((kSplit ? done : done >> 1) & 1u) ^ 1u, gave_up, a.polls);
           tc_fence_after();
           const uint32_t acc = tmem + buf * kTok;
           const uint32_t idesc = instr_desc(std::is_same<T, __nv_bfloat16>::value, kMode != kForward, kMode == kGradW,
@@ -637,7 +638,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
           ++done;
         }
         // the next tile is found while this one's products run
-        if (tile < tiles - step) t = tile_of<kMode, kTok, kGated>(a, table, tile + step, half);
+        if (tile < tiles - step) t = tile_of<kMode, kTok, kGated, kSplit>(a, table, tile + step, half);
       }
       if (!ok) {  // the products in flight end before their tensor memory is freed
         mma_commit<kPair>(drained);
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
     uint32_t next = 0, phases = 0;  // the tile's first stage; a parity per stage
     bool ok = true;
     for (int tile = first; ok && tile < tiles; tile += step) {
-      const Tile t = tile_of<kMode, kTok, kGated>(a, table, tile, half);
+      const Tile t = tile_of<kMode, kTok, kGated, kSplit>(a, table, tile, half);
       next += t.chunks;
       const int left = t.n & (kDepth - 1);
       if (left == 0) continue;
@@ -670,14 +671,14 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
       __syncwarp();
       if (lane == 0) arrive_at<true>(in_block(full + s, 0));
     }
-  } else if (!S::kSplit) {
+  } else if (!kSplit) {
     // Two warps share a quarter of the lanes and take every other 32 columns.
     const int quarter = warp & 3, part = (warp - 2) >> 2;
     const uint32_t base = smem_u32(staging) + (warp - 2) * 32 * kPitch;
     uint32_t done = 0;
     bool ok = true;
     for (int tile = first; tile < tiles; tile += step) {
-      const Tile t = tile_of<kMode, kTok, kGated>(a, table, tile, half);
+      const Tile t = tile_of<kMode, kTok, kGated, kSplit>(a, table, tile, half);
       const int feat0 = t.f0 + quarter * (S::kFeat / 4);
       const uint32_t buf = done & 1u;
       const bool sums = t.chunks > 0;
@@ -728,13 +729,13 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated>::kThreads, Shape<kM
     }
   }
 
-  if constexpr (S::kSplit) {
+  if constexpr (kSplit) {
     // one tile per cluster: the ranks' partials meet in shared memory
     __syncwarp();
     cluster_wait();  // every block has started
     const bool busy = first < tiles;  // the same for all ranks of the cluster
     if (busy) {
-      const Tile t = tile_of<kMode, kTok, kGated>(a, table, first, 0);
+      const Tile t = tile_of<kMode, kTok, kGated, kSplit>(a, table, first, 0);
       int s0, s1;
       share(t, s0, s1);
       const int quarter = warp & 3;
@@ -842,19 +843,19 @@ cudaError_t map_gated(CUtensorMap* m, const void* base, int64_t in, int64_t out,
   return encode(m, base, 5, dims, strides, box);
 }
 
-template <typename T, int kMode, int kTok, bool kGated>
+template <typename T, int kMode, int kTok, bool kGated, bool kSplit = false>
 cudaError_t allow_smem() {
-  return cudaFuncSetAttribute(k_product<T, kMode, kTok, kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Shape<kMode, kTok, kGated>::kSmem);
+  return cudaFuncSetAttribute(k_product<T, kMode, kTok, kGated, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Shape<kMode, kTok, kGated, kSplit>::kSmem);
 }
 
-template <typename T, int kMode, int kTok, bool kGated>
+template <typename T, int kMode, int kTok, bool kGated, bool kSplit = false>
 cudaError_t launch(const char* name, const CUtensorMap& mf, const CUtensorMap& mt, const CUtensorMap& full, const Args& a,
                    int64_t grid, int cluster, int tiles_grad_w, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(Shape<kMode, kTok, kGated>::kThreads);
-  cfg.dynamicSmemBytes = Shape<kMode, kTok, kGated>::kSmem;
+  cfg.blockDim = dim3(Shape<kMode, kTok, kGated, kSplit>::kThreads);
+  cfg.dynamicSmemBytes = Shape<kMode, kTok, kGated, kSplit>::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -866,7 +867,7 @@ cudaError_t launch(const char* name, const CUtensorMap& mf, const CUtensorMap& m
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   Launch guard(name, st);
-  return cudaLaunchKernelEx(&cfg, k_product<T, kMode, kTok, kGated>, mf, mt, full, a, tiles_grad_w);
+  return cudaLaunchKernelEx(&cfg, k_product<T, kMode, kTok, kGated, kSplit>, mf, mt, full, a, tiles_grad_w);
 }
 
 // Forward and input gradient: the form by the mean number of rows of an expert
@@ -884,23 +885,25 @@ cudaError_t launch_rows(const char* name, const CUtensorMap& mf, const void* x, 
   auto bound = [&](int tok, int feat) {
     return (std::min<int64_t>(a.experts + 1, a.rows) + a.rows / tok) * ((a.feat + feat - 1) / feat);
   };
-  const int64_t pairs = bound(256, Shape<kMode, 256, kGated>::kTileFeat);
+  constexpr int kWide = kGated ? 64 : 128;  // features of a block's tile
+  const int64_t pairs = bound(256, 2 * kWide);
   CUtensorMap mt, full;
   cudaError_t e = map_rows(&mt, x, a.depth, a.rows, x_stride, kTokBox);
   if (e != cudaSuccess) return e;
   if (mean <= 16 || (mean <= 128 && 2 * pairs <= sms)) {
-    const int64_t tiles = bound(32, Shape<kMode, 32, kGated>::kTileFeat);
+    const int64_t tiles = bound(32, kWide);
     const int chunks = (a.depth + kDepth - 1) / kDepth;
     int ranks = 1;
     while (ranks < 8 && tiles * ranks * 2 <= 2 * sms && chunks >= 8 * ranks) ranks *= 2;
     static_assert(kTokBox == 32, "a full tile is one small box");
-    return launch<T, kMode, 32, kGated>(name, mf, mt, mt, a, tiles * ranks, ranks, 0, st);
+    if (ranks == 1) return launch<T, kMode, 32, kGated>(name, mf, mt, mt, a, std::min<int64_t>(tiles, 2 * sms), 1, 0, st);
+    return launch<T, kMode, 32, kGated, true>(name, mf, mt, mt, a, tiles * ranks, ranks, 0, st);
   }
   e = map_rows(&full, x, a.depth, a.rows, x_stride, 128);  // the tokens of a full tile, of one block
   if (e != cudaSuccess) return e;
   if (mean > 64 && (mean <= 128 || 4 * pairs <= sms))
     return launch<T, kMode, 128, kGated>(
-        name, mf, mt, full, a, std::min<int64_t>(bound(128, Shape<kMode, 128, kGated>::kTileFeat), sms), 1, 0, st);
+        name, mf, mt, full, a, std::min<int64_t>(bound(128, kWide), sms), 1, 0, st);
   return launch<T, kMode, 256, kGated>(name, mf, mt, full, a, 2 * std::min<int64_t>(pairs, sms / 2), 2, 0, st);
 }
 
@@ -927,6 +930,8 @@ cudaError_t init_as() {
   if (!fn || got != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
   g_encode = reinterpret_cast<EncodeTiled>(fn);
   for (cudaError_t r : {allow_smem<T, kForward, 32, false>(), allow_smem<T, kForward, 32, true>(),
+                        allow_smem<T, kForward, 32, false, true>(), allow_smem<T, kForward, 32, true, true>(),
+                        allow_smem<T, kGradX, 32, false, true>(),
                         allow_smem<T, kForward, 128, false>(), allow_smem<T, kForward, 128, true>(),
                         allow_smem<T, kForward, 256, false>(), allow_smem<T, kForward, 256, true>(),
                         allow_smem<T, kGradX, 32, false>(), allow_smem<T, kGradX, 128, false>(),
