@@ -872,10 +872,10 @@ cudaError_t launch(const char* name, const CUtensorMap& mf, const CUtensorMap& m
 
 // Forward and input gradient: the form by the mean number of rows of an expert
 // that can have any, and by whether pairs would fill the GPU.  Measured (us,
-// forward, 64 experts, 2048 -> 2048): 24 rows few 102, many 96; 64 rows some 100,
-// many 98 (input gradient 107, 96); 128 rows some 104, many 108 (102, 112).  One
-// matrix, few pairs: 40 rows 4096 -> 4096 many 31, few 23; 100 rows some 38, few
-// 31; 512 rows 2048 -> 2048 many 24, some 21.
+// forward, 64 experts, 2048 -> 2048): 24 rows few 90, many 96; 48 rows few 104,
+// many 98; 64 rows some 100, many 98; 128 rows some 102, many 108.  One matrix,
+// few pairs: 40 rows 4096 -> 4096 many 31, few 23; 100 rows some 38, few 31; 512
+// rows 2048 -> 2048 many 24, some 21.
 template <typename T, int kMode, bool kGated>
 cudaError_t launch_rows(const char* name, const CUtensorMap& mf, const void* x, int64_t x_stride, const Args& a, int sms,
                         cudaStream_t st) {
@@ -890,7 +890,7 @@ cudaError_t launch_rows(const char* name, const CUtensorMap& mf, const void* x, 
   CUtensorMap mt, full;
   cudaError_t e = map_rows(&mt, x, a.depth, a.rows, x_stride, kTokBox);
   if (e != cudaSuccess) return e;
-  if (mean <= 16 || (mean <= 128 && 2 * pairs <= sms)) {
+  if (mean <= 32 || (mean <= 128 && 2 * pairs <= sms)) {
     const int64_t tiles = bound(32, kWide);
     const int chunks = (a.depth + kDepth - 1) / kDepth;
     int ranks = 1;
