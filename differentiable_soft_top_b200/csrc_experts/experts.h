@@ -22,7 +22,7 @@ struct RouteFwd {
   int32_t* chosen;
   bool vec, bias_vec;  // set by the launcher
 };
-cudaError_t launch_route_fwd(RouteFwd a, int sms, cudaStream_t st);
+cudaError_t launch_route_fwd(RouteFwd a, cudaStream_t st);
 
 struct RouteBwd {
   const void* scores;
@@ -39,7 +39,7 @@ struct RouteBwd {
   int64_t grad_stride;
   bool vec, bias_vec, grad_vec;  // set by the launcher
 };
-cudaError_t launch_route_bwd(RouteBwd a, int sms, cudaStream_t st);
+cudaError_t launch_route_bwd(RouteBwd a, cudaStream_t st);
 
 size_t plan_workspace(int64_t slots, int experts);
 cudaError_t launch_plan(const int32_t* chosen, int64_t slots, int experts, int32_t* offsets, int32_t* rows,

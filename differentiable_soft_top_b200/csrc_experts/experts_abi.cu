@@ -131,11 +131,10 @@ int lapsum_experts_route_fwd(const void* scores, int dtype, int64_t tokens, int 
   if (overlaps(scores, in, weights, out) || overlaps(scores, in, chosen, out) || overlaps(weights, out, chosen, out) ||
       overlaps(bias, 4 * (size_t)experts, weights, out) || overlaps(bias, 4 * (size_t)experts, chosen, out))
     return LAPSUM_EINVAL;
-  const int sms = device_sms();
-  if (!sms) return LAPSUM_ECUDA;
+  if (!device_sms()) return LAPSUM_ECUDA;
   RouteFwd a{scores, dtype, tokens, row_stride, experts, k, score, bias, groups, groups_kept, group_top,
              renormalize != 0, scale, weights, chosen, false, false};
-  return done(launch_route_fwd(a, sms, (cudaStream_t)stream));
+  return done(launch_route_fwd(a, (cudaStream_t)stream));
 }
 
 int lapsum_experts_route_bwd(const void* scores, int dtype, int64_t tokens, int experts, int64_t row_stride, int k,
@@ -153,11 +152,10 @@ int lapsum_experts_route_bwd(const void* scores, int dtype, int64_t tokens, int 
       overlaps(chosen, small, grad_scores, out) || overlaps(weights, small, grad_scores, out) ||
       overlaps(grad_weights, small, grad_scores, out) || overlaps(bias, 4 * (size_t)experts, grad_scores, out))
     return LAPSUM_EINVAL;
-  const int sms = device_sms();
-  if (!sms) return LAPSUM_ECUDA;
+  if (!device_sms()) return LAPSUM_ECUDA;
   RouteBwd a{scores, dtype, tokens, row_stride, experts, k, score, bias, renormalize != 0, scale, chosen, weights,
              grad_weights, grad_scores, grad_stride, false, false, false};
-  return done(launch_route_bwd(a, sms, (cudaStream_t)stream));
+  return done(launch_route_bwd(a, (cudaStream_t)stream));
 }
 
 size_t lapsum_experts_plan_workspace_size(int64_t slots, int experts) {

