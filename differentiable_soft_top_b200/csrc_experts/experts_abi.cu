@@ -463,15 +463,18 @@ int lapsum_experts_linear_bwd(const void* grad_y, int dtype, int64_t rows, int64
 // Workspace of the layer: the plan's arrays and scratch, then the rows before,
 // between and after the products, each on a 256-byte boundary.
 struct MlpLayout {
-  size_t offsets, rows, slots, plan, x_rows, h, y, total;
+  size_t offsets, rows, slots, plan, x_rows, pre, h, y, total;
+  int64_t hidden;
 };
-static MlpLayout mlp_layout(int64_t tokens, int k, int experts, int64_t dim, int64_t hidden, int64_t dim_out) {
+static MlpLayout mlp_layout(int64_t tokens, int k, int experts, int64_t dim, int64_t up, int activation, int64_t dim_out,
+                            bool keep) {
   const size_t n = (size_t)tokens * k;
   MlpLayout l;
+  l.hidden = activation == LAPSUM_ACT_SWIGLU ? up / 2 : up;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
-    at = (at + bytes + 255) & ~size_t(255);
+    at = round256(at + bytes);
     return here;
   };
   l.offsets = take(4 * ((size_t)experts + 1));
@@ -479,43 +482,48 @@ static MlpLayout mlp_layout(int64_t tokens, int k, int experts, int64_t dim, int
   l.slots = take(4 * n);
   l.plan = take(plan_workspace((int64_t)n, experts));
   l.x_rows = take(2 * n * dim);
-  l.h = take(2 * n * hidden);
+  l.pre = take(keep && activation != LAPSUM_ACT_NONE ? 2 * n * up : 0);
+  l.h = take(2 * n * l.hidden);
   l.y = take(2 * n * dim_out);
   l.total = at;
   return l;
 }
-static bool mlp_shape(int64_t tokens, int k, int experts, int64_t dim, int64_t hidden, int64_t dim_out) {
-  return tokens >= 1 && k >= 1 && k <= LAPSUM_EXPERTS_MAX_K && tokens <= (kMaxIndex - 1024) / k && experts >= 1 &&
-         experts <= LAPSUM_EXPERTS_MAX && dim >= 1 && hidden >= 1 && dim_out >= 1 && dim <= (1 << 24) &&
-         hidden <= (1 << 24) && dim_out <= (1 << 24);
+static int mlp_shape(int dtype, int64_t tokens, int k, int experts, int64_t dim, int64_t up, int activation,
+                     int64_t dim_out) {
+  if (activation < LAPSUM_ACT_NONE || activation > LAPSUM_ACT_SWIGLU) return LAPSUM_EINVAL;
+  const bool gated = activation == LAPSUM_ACT_SWIGLU;
+  if (tokens < 1 || k < 1 || k > LAPSUM_EXPERTS_MAX_K || tokens > (kMaxIndex - 1024) / k || experts < 1 ||
+      experts > LAPSUM_EXPERTS_MAX || up < 1 || (gated && up % 16))
+    return LAPSUM_EINVAL;
+  const int64_t n = tokens * k, hidden = gated ? up / 2 : up;
+  if (!linear_shape(dtype, n, dim, up) || !linear_shape(dtype, n, hidden, dim_out)) return LAPSUM_EINVAL;
+  if (!tiles_fit(n, experts, dim, up) || !tiles_fit(n, experts, hidden, dim_out)) return LAPSUM_ETOOLARGE;
+  return LAPSUM_OK;
 }
 
-size_t lapsum_experts_mlp_workspace_size(int64_t tokens, int k, int experts, int64_t dim, int64_t hidden,
-                                         int64_t dim_out) {
-  if (!mlp_shape(tokens, k, experts, dim, hidden, dim_out)) return 0;
-  return mlp_layout(tokens, k, experts, dim, hidden, dim_out).total;
+size_t lapsum_experts_mlp_workspace_size(int64_t tokens, int k, int experts, int64_t dim, int64_t up, int activation,
+                                         int64_t dim_out, int keep) {
+  if (mlp_shape(LAPSUM_BF16, tokens, k, experts, dim, up, activation, dim_out) != LAPSUM_OK) return 0;
+  return mlp_layout(tokens, k, experts, dim, up, activation, dim_out, keep != 0).total;
 }
 
 int lapsum_experts_mlp_fwd(const void* x, int dtype, int64_t tokens, int64_t dim, int64_t x_stride, const float* weights,
                            const int32_t* chosen, int k, const void* w_in, const void* b_in, int experts, int64_t up,
                            int activation, const void* w_out, const void* b_out, int64_t dim_out, const void* residual,
-                           int64_t residual_stride, void* out, int64_t out_stride, uint32_t* status, void* workspace,
-                           size_t workspace_bytes, void* stream) {
-  const bool gated = activation == LAPSUM_ACT_SWIGLU;
-  if (activation < LAPSUM_ACT_NONE || activation > LAPSUM_ACT_SWIGLU || up < 1 || (gated && up % 16)) return LAPSUM_EINVAL;
-  const int64_t hidden = gated ? up / 2 : up;
-  if (!mlp_shape(tokens, k, experts, dim, hidden, dim_out)) return LAPSUM_EINVAL;
-  const int64_t n = tokens * k;
+                           int64_t residual_stride, void* out, int64_t out_stride, int keep, uint32_t* status,
+                           void* workspace, size_t workspace_bytes, void* stream) {
   // everything that a later step could refuse is checked before the first is enqueued
-  if (!linear_shape(dtype, n, dim, up) || !linear_shape(dtype, n, hidden, dim_out)) return LAPSUM_EINVAL;
-  if (!tiles_fit(n, experts, dim, up) || !tiles_fit(n, experts, hidden, dim_out)) return LAPSUM_ETOOLARGE;
+  int rc = mlp_shape(dtype, tokens, k, experts, dim, up, activation, dim_out);
+  if (rc != LAPSUM_OK) return rc;
+  const int64_t n = tokens * k;
   if (!x || !weights || !chosen || !w_in || !w_out || !out || x_stride < dim || out_stride < dim_out ||
       (residual && residual_stride < dim_out))
     return LAPSUM_EINVAL;
   if (!aligned(x, 2) || !aligned(out, 2) || !aligned(residual, 2) || !aligned(weights, 4) || !aligned(chosen, 4) ||
       !aligned(w_in, 16) || !aligned(w_out, 16) || !aligned(b_in, 2) || !aligned(b_out, 2) || !aligned(status, 4))
     return LAPSUM_EINVAL;
-  const MlpLayout l = mlp_layout(tokens, k, experts, dim, hidden, dim_out);
+  const MlpLayout l = mlp_layout(tokens, k, experts, dim, up, activation, dim_out, keep != 0);
+  const int64_t hidden = l.hidden;
   if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256)) return LAPSUM_EWORKSPACE;
   struct {
     const void* p;
@@ -537,18 +545,97 @@ int lapsum_experts_mlp_fwd(const void* x, int dtype, int64_t tokens, int64_t dim
   auto* offsets = reinterpret_cast<int32_t*>(ws + l.offsets);
   auto* rows = reinterpret_cast<int32_t*>(ws + l.rows);
   auto* slots = reinterpret_cast<int32_t*>(ws + l.slots);
-  int rc = lapsum_experts_plan(chosen, n, experts, offsets, rows, slots, ws + l.plan, l.x_rows - l.plan, stream);
+  void* pre = keep && activation != LAPSUM_ACT_NONE ? ws + l.pre : nullptr;
+  rc = lapsum_experts_plan(chosen, n, experts, offsets, rows, slots, ws + l.plan, l.x_rows - l.plan, stream);
   if (rc == LAPSUM_OK)
     rc = lapsum_experts_dispatch(x, dtype, tokens, k, dim, x_stride, slots, ws + l.x_rows, dim, stream);
   if (rc == LAPSUM_OK)
     rc = lapsum_experts_linear_fwd(ws + l.x_rows, dtype, n, dim, dim, w_in, experts, up, offsets, b_in, activation,
-                                   nullptr, 0, ws + l.h, hidden, nullptr, 0, status, stream);
+                                   nullptr, 0, ws + l.h, hidden, pre, up, status, stream);
   if (rc == LAPSUM_OK)
     rc = lapsum_experts_linear_fwd(ws + l.h, dtype, n, hidden, hidden, w_out, experts, dim_out, offsets, b_out,
                                    LAPSUM_ACT_NONE, nullptr, 0, ws + l.y, dim_out, nullptr, 0, status, stream);
   if (rc == LAPSUM_OK)
     rc = lapsum_experts_combine(ws + l.y, dtype, tokens, k, dim_out, dim_out, weights, rows, residual, residual_stride,
                                 out, out_stride, stream);
+  return rc;
+}
+
+// Scratch of the layer's backward: the rows' gradients and the products' own.
+struct MlpBwdLayout {
+  size_t gy, gh, gx, products, total;
+};
+static MlpBwdLayout mlp_bwd_layout(int64_t n, int experts, int64_t dim, int64_t up, int activation, int64_t dim_out) {
+  MlpBwdLayout l;
+  const int64_t hidden = activation == LAPSUM_ACT_SWIGLU ? up / 2 : up;
+  l.gy = 0;
+  l.gh = round256(2 * (size_t)n * dim_out);
+  l.gx = l.gh + round256(2 * (size_t)n * hidden);
+  l.products = l.gx + round256(2 * (size_t)n * dim);
+  l.total = l.products + std::max(lapsum_experts_linear_bwd_workspace_size(n, experts, dim_out, LAPSUM_ACT_NONE, 1),
+                                  lapsum_experts_linear_bwd_workspace_size(n, experts, up, activation, 1));
+  return l;
+}
+
+size_t lapsum_experts_mlp_bwd_workspace_size(int64_t tokens, int k, int experts, int64_t dim, int64_t up, int activation,
+                                             int64_t dim_out) {
+  if (mlp_shape(LAPSUM_BF16, tokens, k, experts, dim, up, activation, dim_out) != LAPSUM_OK) return 0;
+  return mlp_bwd_layout(tokens * k, experts, dim, up, activation, dim_out).total;
+}
+
+int lapsum_experts_mlp_bwd(const void* grad, int dtype, int64_t tokens, int64_t dim, int64_t grad_stride,
+                           const float* weights, int k, const void* w_in, int experts, int64_t up, int activation,
+                           const void* w_out, int64_t dim_out, const void* kept, int residual_is_x, void* grad_x,
+                           float* grad_weights, void* grad_w_in, void* grad_b_in, void* grad_w_out, void* grad_b_out,
+                           uint32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = mlp_shape(dtype, tokens, k, experts, dim, up, activation, dim_out);
+  if (rc != LAPSUM_OK) return rc;
+  const int64_t n = tokens * k;
+  const bool inner = grad_x || grad_w_in || grad_b_in, outer = inner || grad_w_out || grad_b_out;
+  if (!grad || !weights || !w_in || !w_out || !kept || grad_stride < dim_out || (!outer && !grad_weights)) return LAPSUM_EINVAL;
+  if (residual_is_x && dim != dim_out) return LAPSUM_EINVAL;
+  if (!aligned(grad, 2) || !aligned(weights, 4) || !aligned(w_in, 16) || !aligned(w_out, 16) || !aligned(kept, 256) ||
+      !aligned(grad_x, 16) || !aligned(grad_weights, 4) || !aligned(grad_w_in, 16) || !aligned(grad_b_in, 2) ||
+      !aligned(grad_w_out, 16) || !aligned(grad_b_out, 2) || !aligned(status, 4))
+    return LAPSUM_EINVAL;
+  const MlpLayout l = mlp_layout(tokens, k, experts, dim, up, activation, dim_out, true);
+  const MlpBwdLayout b = mlp_bwd_layout(n, experts, dim, up, activation, dim_out);
+  const int64_t hidden = l.hidden;
+  if (!workspace || workspace_bytes < b.total || !aligned(workspace, 256)) return LAPSUM_EWORKSPACE;
+  const size_t wi = 2 * (size_t)experts * up * dim, wo = 2 * (size_t)experts * dim_out * hidden;
+  struct {
+    const void* p;
+    size_t n;
+  } outs[7] = {{grad_x, 2 * (size_t)tokens * dim}, {grad_weights, 4 * (size_t)n}, {grad_w_in, wi},
+               {grad_b_in, 2 * (size_t)experts * up}, {grad_w_out, wo}, {grad_b_out, 2 * (size_t)experts * dim_out},
+               {workspace, b.total}},
+    ins[5] = {{grad, span(tokens, dim_out, grad_stride, 2)}, {weights, 4 * (size_t)n}, {w_in, wi}, {w_out, wo}, {kept, l.total}};
+  for (int o = 0; o < 7; ++o) {
+    for (const auto& i : ins)
+      if (overlaps(outs[o].p, outs[o].n, i.p, i.n)) return LAPSUM_EINVAL;
+    for (int q = 0; q < o; ++q)
+      if (overlaps(outs[o].p, outs[o].n, outs[q].p, outs[q].n)) return LAPSUM_EINVAL;
+  }
+  const unsigned char* in = static_cast<const unsigned char*>(kept);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  auto* offsets = reinterpret_cast<const int32_t*>(in + l.offsets);
+  auto* rows = reinterpret_cast<const int32_t*>(in + l.rows);
+  auto* slots = reinterpret_cast<const int32_t*>(in + l.slots);
+  const void* pre = activation != LAPSUM_ACT_NONE ? in + l.pre : nullptr;
+  const size_t left = workspace_bytes - b.products;
+  rc = lapsum_experts_combine_bwd(grad, dtype, tokens, k, dim_out, grad_stride, in + l.y, dim_out, weights, rows, slots,
+                                  outer ? ws + b.gy : nullptr, dim_out, grad_weights, stream);
+  if (rc == LAPSUM_OK && outer)
+    rc = lapsum_experts_linear_bwd(ws + b.gy, dtype, n, dim_out, dim_out, nullptr, in + l.h, hidden, hidden, w_out, experts,
+                                   offsets, LAPSUM_ACT_NONE, inner ? ws + b.gh : nullptr, grad_w_out, grad_b_out, status,
+                                   ws + b.products, left, stream);
+  if (rc == LAPSUM_OK && inner)
+    rc = lapsum_experts_linear_bwd(ws + b.gh, dtype, n, up, hidden, pre, in + l.x_rows, dim, dim, w_in, experts, offsets,
+                                   activation, grad_x ? ws + b.gx : nullptr, grad_w_in, grad_b_in, status,
+                                   ws + b.products, left, stream);
+  if (rc == LAPSUM_OK && grad_x)
+    rc = lapsum_experts_combine(ws + b.gx, dtype, tokens, k, dim, dim, nullptr, rows, residual_is_x ? grad : nullptr,
+                                grad_stride, grad_x, dim, stream);
   return rc;
 }
 

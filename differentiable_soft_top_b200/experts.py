@@ -81,7 +81,9 @@ def _load():
                 "linear_dx": [P, i32, i64, i64, i64, P, i32, i64, P, P, i64, P, P],
                 "linear_dweight": [P, i32, i64, i64, i64, P, i64, i64, i32, P, P, P, P],
                 "linear_bwd": [P, i32, i64, i64, i64, P, P, i64, i64, P, i32, P, i32, P, P, P, P, P, sz, P],
-                "mlp_fwd": [P, i32, i64, i64, i64, P, P, i32, P, P, i32, i64, i32, P, P, i64, P, i64, P, i64, P, P, sz, P],
+                "mlp_fwd": [P, i32, i64, i64, i64, P, P, i32, P, P, i32, i64, i32, P, P, i64, P, i64, P, i64, i32, P, P, sz,
+                            P],
+                "mlp_bwd": [P, i32, i64, i64, i64, P, i32, P, i32, i64, i32, P, i64, P, i32, P, P, P, P, P, P, P, P, sz, P],
                 "trace_collect": [ctypes.c_char_p, sz],
             }.items():
                 fn = getattr(lib, "lapsum_experts_" + name)
@@ -92,7 +94,9 @@ def _load():
             lib.lapsum_experts_linear_act_workspace_size.restype = sz
             lib.lapsum_experts_linear_bwd_workspace_size.argtypes = [i64, i32, i64, i32, i32]
             lib.lapsum_experts_linear_bwd_workspace_size.restype = sz
-            lib.lapsum_experts_mlp_workspace_size.argtypes = [i64, i32, i32, i64, i64, i64]
+            lib.lapsum_experts_mlp_workspace_size.argtypes = [i64, i32, i32, i64, i64, i32, i64, i32]
+            lib.lapsum_experts_mlp_bwd_workspace_size.argtypes = [i64, i32, i32, i64, i64, i32, i64]
+            lib.lapsum_experts_mlp_bwd_workspace_size.restype = sz
             lib.lapsum_experts_mlp_workspace_size.restype = sz
             lib.lapsum_experts_last_cuda_error.argtypes = []
             lib.lapsum_experts_last_cuda_error.restype = ctypes.c_char_p
@@ -464,15 +468,19 @@ def _check_weight(weight, bias, name, x, din, act):
     return e, n
 
 
-def _mlp_fwd(x, weights, chosen, w_in, w_out, b_in, b_out, act, residual, status):
-    """The layer on laid-out tensors, and what its gradient takes."""
-    p = plan(chosen, w_in.shape[0])
+def _mlp_fwd(x, weights, chosen, w_in, w_out, b_in, b_out, act, residual, status, keep):
+    """The layer, and its workspace (with keep: what its gradient takes)."""
     t, k = chosen.shape
-    x_rows = _dispatch(x, p.slots, t, k)
-    h, pre = _linear_fwd(x_rows, w_in, p.offsets, b_in, act, None, act != 0, status)
-    y, _ = _linear_fwd(h, w_out, p.offsets, b_out, 0, None, False, status)
-    out = _combine(y, weights, p.rows, residual)
-    return out, (p.offsets, p.rows, p.slots, x_rows, pre, h, y)
+    (e, up, d), dim = w_in.shape, w_out.shape[1]
+    out = torch.empty((t, dim), dtype=x.dtype, device=x.device)
+    need = _load().lapsum_experts_mlp_workspace_size(t, k, e, d, up, act, dim, keep)
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    if t:
+        _call("mlp_fwd", x.get_device(), x.data_ptr(), _DTYPES[x.dtype], t, d, _stride(x), weights.data_ptr(),
+              chosen.data_ptr(), k, w_in.data_ptr(), _ptr(b_in), e, up, act, w_out.data_ptr(), _ptr(b_out), dim,
+              _ptr(residual), _stride(residual) if residual is not None else 0, out.data_ptr(), dim, keep, _ptr(status),
+              ws.data_ptr(), need)
+    return out, ws
 
 
 def mlp(x, weights, chosen, w_in, w_out, *, b_in=None, b_out=None, activation: str | None = "swiglu", residual=None,
@@ -512,20 +520,9 @@ def mlp(x, weights, chosen, w_in, w_out, *, b_in=None, b_out=None, activation: s
         own = residual is x  # its gradient joins that of x in one pass
         return _function("mlp").apply(x, weights, w_in, w_out, b_in, b_out, None if own else residual, own, chosen, act,
                                       status)
-    out = torch.empty((t, dim), dtype=x.dtype, device=dev)
-    if t == 0:
-        return out
-    x, w_in, w_out, weights = _rows_of(x), _dense16(w_in), _dense16(w_out), weights.contiguous()
-    b_in = None if b_in is None else b_in.contiguous()
-    b_out = None if b_out is None else b_out.contiguous()
-    residual = None if residual is None else _rows_of(residual)
-    need = _load().lapsum_experts_mlp_workspace_size(t, k, e, x.shape[1], w_out.shape[2], dim)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _call("mlp_fwd", x.get_device(), x.data_ptr(), _DTYPES[x.dtype], t, x.shape[1], _stride(x), weights.data_ptr(),
-          chosen.data_ptr(), k, w_in.data_ptr(), _ptr(b_in), e, up, act, w_out.data_ptr(), _ptr(b_out), dim,
-          _ptr(residual), _stride(residual) if residual is not None else 0, out.data_ptr(), dim, _ptr(status),
-          ws.data_ptr(), need)
-    return out
+    return _mlp_fwd(_rows_of(x), weights.contiguous(), chosen, _dense16(w_in), _dense16(w_out),
+                    None if b_in is None else b_in.contiguous(), None if b_out is None else b_out.contiguous(), act,
+                    None if residual is None else _rows_of(residual), status, 0)[0]
 
 
 # ---------------------------------------------------------------------------
@@ -646,27 +643,31 @@ def _make_functions():
             x2, w2, wi, wo = _rows_of(x), weights.contiguous(), _dense16(w_in), _dense16(w_out)
             res = x2 if own else None if residual is None else _rows_of(residual)
             out, kept = _mlp_fwd(x2, w2, chosen, wi, wo, None if b_in is None else b_in.contiguous(),
-                                 None if b_out is None else b_out.contiguous(), act, res, status)
-            ctx.save_for_backward(w2, wi, wo, *kept)
+                                 None if b_out is None else b_out.contiguous(), act, res, status, 1)
+            ctx.save_for_backward(w2, wi, wo, kept)
             ctx.act, ctx.own, ctx.status = act, own, status
             return out
 
         @staticmethod
         def backward(ctx, g):
             _once()
-            weights, w_in, w_out, offsets, rows, slots, x_rows, pre, h, y = ctx.saved_tensors
+            weights, w_in, w_out, kept = ctx.saved_tensors
             need_x, need_w, need_in, need_out, need_bi, need_bo, need_r = ctx.needs_input_grad[:7]
-            status = ctx.status
-            inner = need_x or need_in or need_bi
-            g2 = _rows_of(g)
-            gy, gw = _combine_bwd(g2, y, weights, rows, slots, inner or need_out or need_bo, need_w)
-            gx = gwi = gbi = gwo = gbo = None
-            if gy is not None:
-                gh, gwo, gbo = _linear_bwd(gy, h, w_out, offsets, None, 0, inner, need_out, need_bo, status)
-                if inner:
-                    gr, gwi, gbi = _linear_bwd(gh, x_rows, w_in, offsets, pre, ctx.act, need_x, need_in, need_bi, status)
-                    if need_x:
-                        gx = _combine(gr, None, rows, g2 if ctx.own else None)
+            (t, k), (e, up, d), dim, act = weights.shape, w_in.shape, w_out.shape[1], ctx.act
+            new = w_in.new_zeros if t == 0 else w_in.new_empty
+            gx = new((t, d)) if need_x else None
+            gw = torch.empty_like(weights) if need_w else None
+            gwi = new((e, up, d)) if need_in else None
+            gwo = new(w_out.shape) if need_out else None
+            gbi = new((e, up)) if need_bi else None
+            gbo = new((e, dim)) if need_bo else None
+            if t and any(ctx.needs_input_grad[:6]):
+                g2 = _rows_of(g)
+                need = _load().lapsum_experts_mlp_bwd_workspace_size(t, k, e, d, up, act, dim)
+                ws = torch.empty(need, dtype=torch.uint8, device=g.device)
+                _call("mlp_bwd", g2.get_device(), g2.data_ptr(), _DTYPES[g2.dtype], t, d, _stride(g2), weights.data_ptr(), k,
+                      w_in.data_ptr(), e, up, act, w_out.data_ptr(), dim, kept.data_ptr(), ctx.own, _ptr(gx), _ptr(gw),
+                      _ptr(gwi), _ptr(gbi), _ptr(gwo), _ptr(gbo), _ptr(ctx.status), ws.data_ptr(), need)
             return gx, gw, gwi, gwo, gbi, gbo, g if need_r else None, None, None, None, None
 
     _functions.update(route=Route, dispatch=Dispatch, combine=Combine, linear=Linear, mlp=Mlp)

@@ -232,21 +232,37 @@ LAPSUM_API int lapsum_experts_linear_bwd(const void* grad_y, int dtype, int64_t 
                                          uint32_t* status, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * The layer in one call (forward only): plan, dispatch, product with bias and
- * activation, product with bias, weighted sum with residual, each as above,
- * for x [tokens, dim] (bf16 or fp16), chosen and weights [tokens, k], w_in
- * [experts, up, dim] (up = hidden, or 2 hidden for LAPSUM_ACT_SWIGLU), w_out
- * [experts, dim_out, hidden] and out [tokens, dim_out].  What lies between is in
- * the workspace (lapsum_experts_mlp_workspace_size bytes, 256-byte aligned).
+ * The layer in one call: plan, dispatch, product with bias and activation,
+ * product with bias, weighted sum with residual, each as above, for x [tokens,
+ * dim] (bf16 or fp16), chosen and weights [tokens, k], w_in [experts, up, dim]
+ * (up = hidden, or 2 hidden for LAPSUM_ACT_SWIGLU), w_out [experts, dim_out,
+ * hidden] and out [tokens, dim_out].  What lies between is in the workspace
+ * (lapsum_experts_mlp_workspace_size bytes, 256-byte aligned); with keep != 0 it
+ * holds what lapsum_experts_mlp_bwd takes and must be left as it is until then.
  * x, residual and out have any row stride; the rest is contiguous.
  */
-LAPSUM_API size_t lapsum_experts_mlp_workspace_size(int64_t tokens, int k, int experts, int64_t dim, int64_t hidden,
-                                                    int64_t dim_out);
+LAPSUM_API size_t lapsum_experts_mlp_workspace_size(int64_t tokens, int k, int experts, int64_t dim, int64_t up,
+                                                    int activation, int64_t dim_out, int keep);
 LAPSUM_API int lapsum_experts_mlp_fwd(const void* x, int dtype, int64_t tokens, int64_t dim, int64_t x_stride,
                                       const float* weights, const int32_t* chosen, int k, const void* w_in,
                                       const void* b_in, int experts, int64_t up, int activation, const void* w_out,
                                       const void* b_out, int64_t dim_out, const void* residual,
-                                      int64_t residual_stride, void* out, int64_t out_stride, uint32_t* status,
+                                      int64_t residual_stride, void* out, int64_t out_stride, int keep,
+                                      uint32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its backward for grad [tokens, dim_out] (any row stride): the gradients of x,
+ * of the weights of the choice, of w_in, b_in, w_out and b_out, contiguous, any of
+ * them NULL.  kept is the forward's workspace.  The residual's gradient is grad;
+ * residual_is_x != 0 adds it to grad_x (dim == dim_out).
+ */
+LAPSUM_API size_t lapsum_experts_mlp_bwd_workspace_size(int64_t tokens, int k, int experts, int64_t dim, int64_t up,
+                                                        int activation, int64_t dim_out);
+LAPSUM_API int lapsum_experts_mlp_bwd(const void* grad, int dtype, int64_t tokens, int64_t dim, int64_t grad_stride,
+                                      const float* weights, int k, const void* w_in, int experts, int64_t up,
+                                      int activation, const void* w_out, int64_t dim_out, const void* kept,
+                                      int residual_is_x, void* grad_x, float* grad_weights, void* grad_w_in,
+                                      void* grad_b_in, void* grad_w_out, void* grad_b_out, uint32_t* status,
                                       void* workspace, size_t workspace_bytes, void* stream);
 
 /*

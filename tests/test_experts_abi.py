@@ -174,14 +174,15 @@ def test_linear_backward_rejects_bad_arguments(lib):
 
 
 def test_layer_rejects_bad_arguments(lib):
-    names = "x dtype tokens dim xs w chosen k wi bi experts up act wo bo dim_out res rs out os status ws wsb stream".split()
+    names = "x dtype tokens dim xs w chosen k wi bi experts up act wo bo dim_out res rs out os keep status ws wsb stream".split()
     good = dict(x=at(0), dtype=1, tokens=8, dim=64, xs=64, w=at(1), chosen=at(2), k=2, wi=at(3), bi=at(4), experts=4, up=128,
-                act=4, wo=at(5), bo=at(6), dim_out=72, res=at(7), rs=72, out=at(8), os=72, status=at(9), ws=at(10), wsb=1 << 20,
-                stream=None)
-    need = lib.lapsum_experts_mlp_workspace_size(8, 2, 4, 64, 64, 72)
+                act=4, wo=at(5), bo=at(6), dim_out=72, res=at(7), rs=72, out=at(8), os=72, keep=0, status=at(9), ws=at(10),
+                wsb=1 << 20, stream=None)
+    size = lib.lapsum_experts_mlp_workspace_size
+    need = size(8, 2, 4, 64, 128, 4, 72, 0)
     assert need >= 16 * 2 * (64 + 64 + 72)
-    assert lib.lapsum_experts_mlp_workspace_size(0, 2, 4, 64, 64, 72) == 0
-    assert lib.lapsum_experts_mlp_workspace_size(8, 33, 4, 64, 64, 72) == 0
+    assert size(8, 2, 4, 64, 128, 4, 72, 1) == need + 16 * 2 * 128
+    assert size(0, 2, 4, 64, 128, 4, 72, 0) == 0 and size(8, 33, 4, 64, 128, 4, 72, 0) == 0
     refused(lib.lapsum_experts_mlp_fwd, names, good, [
         (dict(x=None), EINVAL), (dict(w=None), EINVAL), (dict(chosen=None), EINVAL), (dict(wi=None), EINVAL),
         (dict(wo=None), EINVAL), (dict(out=None), EINVAL), (dict(dtype=0), EINVAL), (dict(tokens=0), EINVAL), (dict(k=0), EINVAL),
@@ -189,6 +190,26 @@ def test_layer_rejects_bad_arguments(lib):
         (dict(act=7), EINVAL), (dict(dim_out=70), EINVAL), (dict(os=64), EINVAL), (dict(rs=64), EINVAL), (dict(experts=0), EINVAL),
         (dict(experts=1025), EINVAL), (dict(wi=at(3) + 8), EINVAL), (dict(out=at(0)), EINVAL), (dict(out=at(10) + 256), EINVAL),
         (dict(ws=at(5)), EINVAL), (dict(ws=None), EWORKSPACE), (dict(wsb=need - 1), EWORKSPACE), (dict(ws=at(10) + 16), EWORKSPACE),
+        (dict(wsb=need, keep=1), EWORKSPACE),
+    ])
+
+
+def test_layer_backward_rejects_bad_arguments(lib):
+    names = "g dtype tokens dim gs w k wi experts up act wo dim_out kept own gx gw gwi gbi gwo gbo status ws wsb stream".split()
+    good = dict(g=at(0), dtype=1, tokens=8, dim=64, gs=64, w=at(1), k=2, wi=at(2), experts=4, up=128, act=4, wo=at(3), dim_out=64,
+                kept=at(4), own=1, gx=at(5), gw=at(6), gwi=at(7), gbi=at(8), gwo=at(9), gbo=at(10), status=None, ws=at(11),
+                wsb=1 << 22, stream=None)
+    size = lib.lapsum_experts_mlp_bwd_workspace_size
+    need = size(8, 2, 4, 64, 128, 4, 64)
+    assert need >= 16 * 2 * (64 + 64 + 64 + 128) and size(0, 2, 4, 64, 128, 4, 64) == 0
+    none = dict(gx=None, gw=None, gwi=None, gbi=None, gwo=None, gbo=None)
+    refused(lib.lapsum_experts_mlp_bwd, names, good, [
+        (dict(g=None), EINVAL), (dict(w=None), EINVAL), (dict(wi=None), EINVAL), (dict(wo=None), EINVAL), (dict(kept=None), EINVAL),
+        (none, EINVAL), (dict(dim_out=72, gs=72), EINVAL), (dict(gs=56), EINVAL), (dict(dtype=0), EINVAL), (dict(act=9), EINVAL),
+        (dict(up=120), EINVAL), (dict(k=0), EINVAL), (dict(experts=0), EINVAL), (dict(gx=at(5) + 8), EINVAL),
+        (dict(gwi=at(7) + 8), EINVAL), (dict(kept=at(4) + 16), EINVAL), (dict(gx=at(0)), EINVAL), (dict(gwi=at(2)), EINVAL),
+        (dict(gwo=at(7)), EINVAL), (dict(gw=at(4) + 1024), EINVAL), (dict(ws=at(4)), EINVAL), (dict(ws=None), EWORKSPACE),
+        (dict(wsb=need - 1), EWORKSPACE), (dict(ws=at(11) + 16), EWORKSPACE),
     ])
 
 

@@ -703,6 +703,36 @@ def test_one_call_layer_equals_its_steps():
     assert empty.shape == (0, 64)
 
 
+def test_layer_gradients_equal_those_of_its_steps():
+    """The one-call layer's gradients are, bit for bit, those of the chained operators; every subset of them too."""
+    logits, x, w_in, w_out, k = small_layer(seed=105)
+    b_in, b_out = randn(12, 96, seed=1, dtype=BF16), randn(12, 64, seed=2, dtype=BF16)
+    logits[5] = -INF
+    w, c = ex.route(logits, k)
+    g = randn(96, 64, seed=3, dtype=BF16)
+    base = [x, w, w_in, w_out, b_in, b_out]
+
+    def steps(x, w, w_in, w_out, b_in, b_out, res):
+        p = ex.plan(c, 12)
+        h = ex.linear(ex.dispatch(x, p), w_in, p.offsets, bias=b_in, activation="swiglu")
+        return ex.combine(ex.linear(h, w_out, p.offsets, bias=b_out), w, p, residual=res)
+
+    res = randn(96, 64, seed=4, dtype=BF16).requires_grad_()
+    leaves = [t.detach().requires_grad_() for t in base]
+    want = torch.autograd.grad(steps(*leaves, res), leaves + [res], g)
+    got = torch.autograd.grad(ex.mlp(*leaves[:2], c, *leaves[2:4], b_in=leaves[4], b_out=leaves[5], residual=res), leaves + [res], g)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for mask in (1, 2, 4, 8, 16, 32, 10, 21):
+        some = [t.detach().requires_grad_(bool(mask >> i & 1)) for i, t in enumerate(base)]
+        out = ex.mlp(*some[:2], c, *some[2:4], b_in=some[4], b_out=some[5])
+        part = torch.autograd.grad(out, [t for t in some if t.requires_grad], g)
+        assert all(torch.equal(a, want[i]) for a, i in zip(part, [i for i in range(6) if mask >> i & 1])), mask
+    # x as its own residual: one rounding of the sum of both gradients
+    (both,) = torch.autograd.grad(ex.mlp(leaves[0], w, c, w_in, w_out, b_in=b_in, b_out=b_out, residual=leaves[0]), leaves[0], g)
+    exact = want[0].double() + g.double()
+    assert ((both.double() - exact).abs() <= half_step(BF16) * (exact.abs() + want[0].double().abs()) + 2.0 ** -24).all()
+
+
 def test_every_subset_of_gradients():
     """A leaf that wants no gradient changes nothing for the others."""
     x, w, off, b, res, _ = linear_case(150, 4, 64, 128, "silu", True, True, 9, BF16, seed=111)
