@@ -318,6 +318,13 @@ __device__ __forceinline__ void finish(const Args& a, const Tile& t, int c0, int
         for (int i = 0; i < 16; ++i) v[h][i] += bias[2 * h + (i >> 1 & 1)];
     }
     if (a.preact) {
+      if (std::is_same<T, __half>::value && !kGated && a.activation == LAPSUM_ACT_RELU) {
+        // what is positive stays so when it is rounded: the gradient asks for the sign
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[h][i] = v[h][i] > 0.0f ? fmaxf(v[h][i], 6e-8f) : v[h][i];
+      }
       if (kGated) {
 #pragma unroll
         for (int up = 0; up < 2; ++up) {

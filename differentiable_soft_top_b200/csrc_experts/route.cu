@@ -699,23 +699,24 @@ __global__ void __launch_bounds__(kThreads) k_route_bwd(const RouteBwd a) {
       }
     }
     bad = __any_sync(kAll, bad);
-    const float gw = warp_sum(g * w);
+    // sum g w / scale; with one choice w / scale is 1 and the gradients below 0
+    const float mean = warp_sum(g * (w / a.scale));
     const float s = e >= 0 ? load_score<kDtype>(a.scores, at + e) : 0.0f;
     float d = 0.0f;
     if (a.score == LAPSUM_SCORE_IDENTITY) {
       if (a.renormalize) {
         const float total = warp_sum(e >= 0 ? s : 0.0f);
-        d = total != 0.0f ? (a.scale * g - gw) / total : 0.0f;
+        d = total != 0.0f ? a.scale * ((g - mean) / total) : 0.0f;
       } else {
         d = a.scale * g;
       }
     } else if (a.renormalize) {
-      d = w * (g - gw / a.scale);
+      d = w * (g - mean);
       if (a.score == LAPSUM_SCORE_SIGMOID) d *= 1.0f / (1.0f + expf(s));
     } else if (a.score == LAPSUM_SCORE_SIGMOID) {
       d = g * w / (1.0f + expf(s));
     } else {
-      d = w * (g - gw / a.scale);  // s_j (scale g_j - sum g w), s_j = w_j / scale
+      d = w * (g - mean);  // s_j (scale g_j - sum g w), s_j = w_j / scale
     }
     float v[kPer];
     const int e0 = lane * kPer, n = max(0, min(kPer, a.experts - e0));
@@ -735,7 +736,7 @@ __global__ void __launch_bounds__(kThreads) k_route_bwd(const RouteBwd a) {
         total += v[i];
       }
       total = warp_sum(total);
-      const float by = total > 0.0f ? -gw / total : 0.0f;
+      const float by = total > 0.0f ? -a.scale * mean / total : 0.0f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) v[i] *= by;
     }
