@@ -104,7 +104,7 @@ struct Order<double> {
 };
 
 // What the order of a token's keys rests on; the fp32 bounds need the largest
-// bias and, for scores used as they are, the largest score.
+// bias (in magnitude, of the experts that are not masked).
 struct Keys {
   const void* scores;
   int64_t at;         // the token's first score
@@ -163,6 +163,15 @@ __device__ __forceinline__ void keys_of(const Rule& r, const Keys& in, const flo
   }
 }
 
+// How far a softmax or sigmoid score of at most s can be off in the fp32 keys.
+// exp(x) is within 2 + 1.18 |x| units of 2^-23 and a softmax's x within |x| 2^-24,
+// with |x| <= -log s; the denominator's sum of up to 1024 terms and the quotients
+// add less than 5.5e-6.  Rises with s; scores end at 1.
+__device__ __forceinline__ float score_error(float s) {
+  s = fminf(fmaxf(s, 1e-37f), 1.0f);
+  return s * (5.5e-6f - 2e-7f * __logf(s));
+}
+
 // Clears the keys of the groups that go.  Returns whether the lowest value that
 // stays and the highest that goes are apart by more than fp32's error (kCheck).
 template <typename K, bool kCheck, int kPer>
@@ -212,20 +221,21 @@ __device__ __forceinline__ bool keep_groups(const Rule& r, const Keys& in, const
   const bool stays = g < r.groups && above < r.kept;
   bool certain = true;
   if (kCheck && !r.raw) {
-    // a value is the sum of up to two keys, each within 2^-18 of its score and
+    // a value is the sum of up to two keys, each off by its score's error and
     // 2^-24 of itself, and scores are at most a key plus the largest bias
     const float lo = -warp_max(stays ? -(float)value : -INFINITY);
     const float hi = warp_max(stays || g >= r.groups ? -INFINITY : (float)value);
-    float size = fabsf(lo) + fabsf(hi) + 4.0f * in.bias_max, unit = 7.7e-6f;
-    if (r.score == LAPSUM_SCORE_IDENTITY) {
+    float size = fabsf(lo) + fabsf(hi) + 4.0f * in.bias_max, scores = 0.0f;
+    if (r.score != LAPSUM_SCORE_IDENTITY) {
+      scores = 4.0f * score_error(0.25f * size);  // of four, the error is concave
+    } else {
       float m = 0.0f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
         if (l[i] != -INFINITY) m = fmaxf(m, fabsf(l[i]));
       size = 4.0f * (warp_max(m) + in.bias_max);
-      unit = 2.4e-7f;
     }
-    certain = hi == -INFINITY || lo - hi > unit * size + 1e-37f;
+    certain = hi == -INFINITY || lo - hi > scores + 2.4e-7f * size + 1e-37f;
   }
   if (r.lanes) {
     if (!stays) {
@@ -340,7 +350,10 @@ __device__ __forceinline__ bool choose(const Rule& r, const Keys& in, const floa
           }
           key = s + bias;
           key1 = s1 + bias1;
-          bound = 7.7e-6f * (s + s1);
+          // what was not picked has no higher key than key1, but its score may be
+          // larger, and its error with it: its bias may take nearly all of it away
+          if (lane == r.k - 1) s1 = fmaxf(s1, key1 + in.bias_max);
+          bound = score_error(s) + score_error(s1);
         }
         bound += 2.4e-7f * (fabsf(key) + fabsf(key1)) + 1e-37f;  // the last: flushed subnormals
       }
@@ -559,7 +572,11 @@ __device__ __noinline__ bool order_again(Rule r, Keys in, int* picked, int count
     const int kth = __ffs(__ballot_sync(kAll, e >= 0 && rank == r.k - 1)) - 1;
     const double low = __shfl_sync(kAll, key, kth);
     const double last = __shfl_sync(kAll, key, count - 1), last_s = __shfl_sync(kAll, s, count - 1);
-    certain = low - last > 1e-5 * fabs(last) + 1.6e-5 * fabs(last_s) + 1e-37;
+    // (those others may have larger scores than the last candidate, as in choose)
+    float error = 0.0f;
+    if (r.score != LAPSUM_SCORE_IDENTITY)
+      error = score_error((float)last_s) + score_error((float)fmax(last_s, last + (double)in.bias_max));
+    certain = low - last > 1e-5 * fabs(last) + (double)error + 1e-37;
   }
   __syncwarp();
   if (e >= 0) picked[rank] = e;
@@ -626,11 +643,11 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? 8 : kPer == 16 ? 6 : 3) 
     float w = 0.0f;
     if (fine) {
       float m = 0.0f;
-      if (!r.raw && r.kept < r.groups && a.bias) {
+      if (!kRaw && a.bias) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
           if (l[i] != -INFINITY) m = fmaxf(m, fabsf(b[i]));
-        m = warp_max(m);
+        m = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(m)));  // of values >= 0
       }
       in.bias_max = m;
       if (soft) {

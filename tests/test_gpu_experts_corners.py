@@ -1,0 +1,62 @@
+"""Corners of the expert operators' range against the definitions in 64 bits (B200)."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="no CUDA device")]
+
+from differentiable_soft_top_b200 import experts as ex  # noqa: E402
+from tests.test_gpu_experts import INF, route64  # noqa: E402
+
+F32, BF16, FP16 = torch.float32, torch.bfloat16, torch.float16
+
+
+# ---------------------------------------------------------------------------
+# routing
+# ---------------------------------------------------------------------------
+def same_choice(x, k, score, bias, groups=1, kept=1, top=1):
+    e = ex.route(x, k, score=score, bias=bias, groups=groups, groups_kept=kept, group_top=top)[1]
+    want = route64(x, k, score, bias, groups, kept, top, True, 1.0)[1]
+    wrong = (e.cpu() != want).any(1)
+    assert not wrong.any(), (int(wrong.sum()), wrong.nonzero().flatten()[:5].tolist())
+
+
+def test_route_where_a_bias_takes_a_large_score_away():
+    """The answer is expert 2, whose key of 7.333e-5 is a score of 0.94 less nearly all of it."""
+    x = torch.tensor([[-9.521313667, -9.521381378, 2.819267035]], device="cuda")
+    b = torch.tensor([0.0, 0.0, -0.9436348081], device="cuda")
+    same_choice(x, 1, "sigmoid", b)
+    assert ex.route(x, 1, score="sigmoid", bias=b)[1].item() == 2
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e,k,groups,kept,top", [(3, 1, 1, 1, 1), (40, 1, 1, 1, 1), (40, 5, 1, 1, 1), (64, 8, 8, 3, 2),
+                                                 (300, 30, 1, 1, 1), (300, 32, 1, 1, 1)])
+def test_route_keys_of_small_and_cancelled_scores(score, e, k, groups, kept, top):
+    """Every other expert has a small score and no bias, the rest a larger score and a bias of nearly minus that: all
+    keys lie within a few 1e-8 of one another, the errors of an fp32 score reach from 1e-12 to 1e-7."""
+    g = torch.Generator().manual_seed(e * 7 + k)
+    t = 300
+    l0 = torch.full((e,), -9.5213, dtype=torch.float64)
+    large = torch.arange(e) % 2 == 0 if e > 3 else torch.tensor([False, False, True])
+    l0[large] = torch.randn(int(large.sum()), generator=g, dtype=torch.float64) + 2.0
+    x = l0 + torch.where(large, 1e-6, 1e-4) * torch.randn(t, e, generator=g, dtype=torch.float64)
+    x = x.float()
+    s = torch.sigmoid(l0) if score == "sigmoid" else torch.softmax(l0, 0)
+    aim = float(s[~large][0])
+    bias = torch.where(large, aim - s, 0.0).float()
+    same_choice(x.cuda(), k, score, bias.cuda(), groups, kept, top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("top", [1, 2])
+def test_route_near_ties_of_very_small_scores(score, top):
+    """Scores of 1e-20 to 1e-37 one or two fp32 steps apart, where exp's relative error is largest; a zero bias, as at the
+    start of training, keeps the comparison of the keys themselves."""
+    g = torch.Generator().manual_seed(5)
+    x = -(45.0 + 40.0 * torch.rand(200, 1, generator=g)) * (1 + 2.0 ** -23 * torch.randint(0, 6, (200, 64), generator=g))
+    if score == "softmax":
+        x[:, 0] = 0.0
+    b = torch.zeros(64, device="cuda")
+    same_choice(x.cuda(), 8, score, b)
+    same_choice(x.cuda(), 8, score, b, 8, 3, top)
