@@ -14,7 +14,9 @@ the weights of the choice, at fixed choice.
 mlp() is plan, dispatch, linear, linear, combine in one; each is public.  Like the
 rest of the package: CUDA tensors only, the current stream of the tensors'
 device, no host synchronisation; every call may be captured into a CUDA graph
-(workspaces are allocated per call, never shared).
+(workspaces are allocated per call, never shared).  Gradients are reverse-mode,
+once: forward-mode tangents and create_graph=True raise.  Capture a backward pass
+only while no eager graph of the same leaves is alive.
 """
 from __future__ import annotations
 
@@ -24,6 +26,7 @@ import threading
 from dataclasses import dataclass
 
 import torch
+import torch.autograd.forward_ad as _forward_ad
 
 from . import LAPSUM_ECUDA, LAPSUM_OK, LapsumError, status_string
 
@@ -209,10 +212,14 @@ def _function(name):
 
 
 def _tracked(*ts):
+    """Whether the call goes through its autograd.Function: some input wants a
+    gradient, or carries a forward-mode tangent (which the function refuses)."""
     if torch.is_grad_enabled():
         for t in ts:
             if t is not None and t.requires_grad:
                 return True
+    if getattr(_forward_ad, "_current_level", 0) >= 0:  # else no tangents exist
+        return any(t is not None and _forward_ad.unpack_dual(t).tangent is not None for t in ts)
     return False
 
 

@@ -6,7 +6,7 @@ pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="no CUDA device")]
 
 from differentiable_soft_top_b200 import experts as ex  # noqa: E402
-from tests.test_gpu_experts import INF, route64  # noqa: E402
+from tests.test_gpu_experts import route64, small_layer  # noqa: E402
 
 F32, BF16, FP16 = torch.float32, torch.bfloat16, torch.float16
 
@@ -60,3 +60,28 @@ def test_route_near_ties_of_very_small_scores(score, top):
     b = torch.zeros(64, device="cuda")
     same_choice(x.cuda(), 8, score, b)
     same_choice(x.cuda(), 8, score, b, 8, 3, top)
+
+
+# ---------------------------------------------------------------------------
+# autograd
+# ---------------------------------------------------------------------------
+def test_forward_mode_tangents_are_refused():
+    """No operator returns a result without its tangent."""
+    import torch.autograd.forward_ad as fwd
+    logits, x, w_in, w_out, k = small_layer(seed=5)
+    w, c = ex.route(logits, k)
+    p = ex.plan(c, 12)
+    rows = ex.dispatch(x, p)
+    y = ex.linear(rows, w_out.transpose(1, 2).contiguous(), p.offsets)
+    with fwd.dual_level():
+        def dual(t):
+            return fwd.make_dual(t, torch.ones_like(t))
+        for call in (lambda: ex.route(dual(logits), k), lambda: ex.dispatch(dual(x), p), lambda: ex.combine(y, dual(w), p),
+                     lambda: ex.combine(dual(y), w, p), lambda: ex.linear(dual(rows), w_in, p.offsets),
+                     lambda: ex.linear(rows, dual(w_in), p.offsets), lambda: ex.mlp(dual(x), w, c, w_in, w_out),
+                     lambda: ex.mlp(x, w, c, w_in, w_out, residual=dual(x))):
+            with torch.no_grad(), pytest.raises(NotImplementedError, match="jvp"):
+                call()
+            with pytest.raises(NotImplementedError, match="jvp"):
+                call()
+        assert torch.equal(ex.route(logits, k)[0], w)  # others in a level as usual
