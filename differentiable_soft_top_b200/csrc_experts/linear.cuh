@@ -318,20 +318,17 @@ __device__ __forceinline__ void finish(const Args& a, const Tile& t, int c0, int
         for (int i = 0; i < 16; ++i) v[h][i] += bias[2 * h + (i >> 1 & 1)];
     }
     if (a.preact) {
-      if (std::is_same<T, __half>::value && !kGated && a.activation == LAPSUM_ACT_RELU) {
-        // what is positive stays so when it is rounded: the gradient asks for the sign
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[h][i] = v[h][i] > 0.0f ? fmaxf(v[h][i], 6e-8f) : v[h][i];
-      }
+      // what relu passes stays positive where it is kept (fp16 ends at 2^-24): its
+      // gradient asks for the sign.  Only there: y is the same whether it is kept or not
+      const bool sign = std::is_same<T, __half>::value && !kGated && a.activation == LAPSUM_ACT_RELU;
+      auto kept = [&](float x) { return sign && x > 0.0f ? fmaxf(x, 6e-8f) : x; };
       if (kGated) {
 #pragma unroll
         for (int up = 0; up < 2; ++up) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) f.p[j][h] = pack2<T>(v[h][4 * j + 2 * up], v[h][4 * j + 2 * up + 1]);
+            for (int h = 0; h < 2; ++h) f.p[j][h] = pack2<T>(kept(v[h][4 * j + 2 * up]), kept(v[h][4 * j + 2 * up + 1]));
           put<kGated>(f, base, static_cast<uint16_t*>(a.preact) + up * a.feat, row, a.preact_stride, feat0, a.feat, n, own,
                       lane);
         }
@@ -340,7 +337,7 @@ __device__ __forceinline__ void finish(const Args& a, const Tile& t, int c0, int
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int g = 0; g < G; ++g)
-            f.p[j][g] = pack2<T>(v[g >> 1][4 * j + 2 * (g & 1)], v[g >> 1][4 * j + 2 * (g & 1) + 1]);
+            f.p[j][g] = pack2<T>(kept(v[g >> 1][4 * j + 2 * (g & 1)]), kept(v[g >> 1][4 * j + 2 * (g & 1) + 1]));
         put<kGated>(f, base, a.preact, row, a.preact_stride, feat0, a.feat, n, own, lane);
       }
     }

@@ -85,3 +85,28 @@ def test_forward_mode_tangents_are_refused():
             with pytest.raises(NotImplementedError, match="jvp"):
                 call()
         assert torch.equal(ex.route(logits, k)[0], w)  # others in a level as usual
+
+
+# ---------------------------------------------------------------------------
+# products
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("r", [4, 70, 600])
+def test_keeping_gradients_does_not_change_relu(dtype, r):
+    """Pre-activations from 2^-40 to 2^-20: with and without gradients the result is the same, rounded once, and the
+    gradient passes wherever they are positive."""
+    g = torch.Generator("cuda").manual_seed(r)
+    x = torch.zeros(r, 64, device="cuda")
+    x[:, 0] = 2.0 ** torch.randint(-24, -14, (r,), generator=g, device="cuda")  # exact in both types: one product each
+    w = torch.zeros(128, 64, device="cuda")
+    w[:, 0] = torch.randn(128, generator=g, device="cuda").sign() * 2.0 ** torch.randint(-14, -5, (128,), generator=g, device="cuda")
+    x, w = x.to(dtype), w.to(dtype)
+    h = x[:, :1].double() * w[:, 0].double()
+    plain = ex.linear(x, w, activation="relu")
+    tracked = ex.linear(x.requires_grad_(), w.requires_grad_(), activation="relu")
+    assert torch.equal(plain, h.clamp_min(0).to(dtype)) and torch.equal(tracked, plain)
+    (dx,) = torch.autograd.grad(tracked, x, torch.ones_like(tracked))
+    want = (h > 0).double() @ w.double()
+    u = torch.finfo(dtype).eps / 2
+    # the sum of at most 128 terms in fp32 and a rounding
+    assert ((dx.double() - want).abs() <= u * want.abs() + 128 * 2.0 ** -24 * (w.double().abs().sum(0)) + 2.0 ** -25).all()
