@@ -147,8 +147,9 @@ __global__ void __launch_bounds__(kThreads, kGated ? 1 : 4) k_act_bwd(const ActA
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float s = sigmoid_of(h[i]);
-              d[i] = g[i] * u[i] * s * fmaf(h[i], 1.0f - s, 1.0f);
-              u[i] = g[i] * h[i] * s;
+              // (factors that vanish first: a large g u must not meet a 0 as infinity)
+              d[i] = g[i] * (s * fmaf(h[i], 1.0f - s, 1.0f)) * u[i];
+              u[i] = g[i] * (h[i] * s);
               s0[i] += d[i];
               s1[i] += u[i];
             }

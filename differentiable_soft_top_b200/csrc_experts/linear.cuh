@@ -321,7 +321,13 @@ __device__ __forceinline__ void finish(const Args& a, const Tile& t, int c0, int
       // what relu passes stays positive where it is kept (fp16 ends at 2^-24): its
       // gradient asks for the sign.  Only there: y is the same whether it is kept or not
       const bool sign = std::is_same<T, __half>::value && !kGated && a.activation == LAPSUM_ACT_RELU;
-      auto kept = [&](float x) { return sign && x > 0.0f ? fmaxf(x, 6e-8f) : x; };
+      // and what is finite stays finite: y often is where h is not (silu of -7e4 in
+      // fp16), and an infinity would turn a gradient that vanishes into NaN
+      constexpr float most = std::is_same<T, __half>::value ? 65504.0f : 3.38953139e38f;
+      auto kept = [&](float x) {
+        if (sign && x > 0.0f) x = fmaxf(x, 6e-8f);
+        return fabsf(x) > most && fabsf(x) < INFINITY ? copysignf(most, x) : x;
+      };
       if (kGated) {
 #pragma unroll
         for (int up = 0; up < 2; ++up) {

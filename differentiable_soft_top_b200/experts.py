@@ -443,6 +443,8 @@ def linear(x, weight, offsets=None, *, bias=None, activation: str | None = None,
     activation: None, "relu", "silu", "gelu" (by erf) or "swiglu" (silu of the
     first half of the outputs times the second: out a multiple of 16, the
     result half as wide).  Rows from offsets[-1] on get the residual (0).
+    Gradients take the pre-activation rounded to the type, beyond its range the
+    type's largest value.
 
     status: an int32 [1] tensor into which STATUS_* bits are or'ed (optional)."""
     act = _check_linear(x, weight, offsets, bias, activation, residual, status)

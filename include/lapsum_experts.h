@@ -179,10 +179,13 @@ LAPSUM_API int lapsum_experts_combine_bwd(const void* grad, int dtype, int64_t t
  *   residual    in   [rows, width] or NULL; width is out, or out/2 for
  *                    LAPSUM_ACT_SWIGLU
  *   y           out  [rows, width]
- *   preact      out  [rows, out] h = W_e x_r + b_e rounded to the type (for
+ *   preact      out  [rows, out] h = W_e x_r + b_e rounded to the type (what is
+ *                    finite stays so, as the type's largest value; for
  *                    LAPSUM_ACT_RELU what is positive stays positive), which
  *                    the backward pass takes (rows from offsets[experts] on
- *                    are left as they were); or NULL.  y does not depend on it
+ *                    are left as they were); or NULL.  y does not depend on it.
+ *                    Where a factor of LAPSUM_ACT_SWIGLU lies beyond the type's
+ *                    range, its gradients are those of the largest value
  *   status      i/o  uint32 [1] or NULL: LAPSUM_EXPERTS_* bits are or'ed in
  */
 LAPSUM_API int lapsum_experts_linear_fwd(const void* x, int dtype, int64_t rows, int64_t in, int64_t x_stride,

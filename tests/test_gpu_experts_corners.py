@@ -110,3 +110,56 @@ def test_keeping_gradients_does_not_change_relu(dtype, r):
     u = torch.finfo(dtype).eps / 2
     # the sum of at most 128 terms in fp32 and a rounding
     assert ((dx.double() - want).abs() <= u * want.abs() + 128 * 2.0 ** -24 * (w.double().abs().sum(0)) + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "swiglu"])
+@pytest.mark.parametrize("r", [12, 300])
+def test_gradients_where_a_pre_activation_leaves_the_type(dtype, act, r):
+    """|h| up to 2^18, beyond fp16: gradients are finite and those of the definition, of h clamped to the type's range
+    (which changes only swiglu's, by its factor).  All values are powers of two, exact in the type where they fit."""
+    f, most = 64, torch.finfo(dtype).max
+    g = torch.Generator("cuda").manual_seed(r)
+
+    def powers(n, lo, hi):
+        sign = torch.randint(0, 2, (n,), generator=g, device="cuda") * 2.0 - 1.0
+        return sign * 2.0 ** torch.randint(lo, hi + 1, (n,), generator=g, device="cuda")
+
+    n = 2 * f if act == "swiglu" else f
+    x, w = torch.zeros(r, 8, device="cuda"), torch.zeros(n, 8, device="cuda")
+    x[:, 0], w[:, 0] = powers(r, 4, 10), powers(n, -12, 8)
+    x, w = x.to(dtype).requires_grad_(), w.to(dtype).requires_grad_()
+    b = torch.zeros(n, dtype=dtype, device="cuda", requires_grad=True)
+    y = ex.linear(x, w, bias=b, activation=act)
+    dy = powers(r * f, -12, -6).view(r, f).to(dtype)
+    got = torch.autograd.grad(y, [x, w, b], dy)
+    h = (x[:, :1].detach().double() * w[:, 0].detach().double()).clamp(-most, most)
+    d = dy.double()
+
+    def silu1(v):
+        s = torch.sigmoid(v)
+        return s * (1 + v * (1 - s))
+
+    if act == "swiglu":
+        a, up = h.chunk(2, 1)
+        dh = torch.cat([d * up * silu1(a), d * a * torch.sigmoid(a)], 1)
+        scale = torch.cat([d * up, d * a], 1).abs()
+    else:
+        d1 = {"relu": lambda: (h > 0).double(), "silu": lambda: silu1(h),
+              "gelu": lambda: 0.5 * torch.erfc(-h * 0.5 ** 0.5) + h * torch.exp(-0.5 * h * h) / (2 * torch.pi) ** 0.5}[act]()
+        dh, scale = d * d1, d.abs()
+    # the derivative within 2^-20 of terms of order 1 (where h is small; beyond it vanishes or is 1), dH rounded, sums
+    u = torch.finfo(dtype).eps / 2
+    e = 2.0 ** -20 * scale.clamp_max(2.0 ** 6) + 2.0 ** -20 * dh.abs()
+    edge = u * dh.abs() + (2.0 ** -25 if dtype == FP16 else 0.0) + e
+    fits = dh.abs().amax() <= most  # else dH itself overflows, as it should
+    assert fits
+    for name, a, ref, tol in (("x", got[0][:, 0], dh @ w[:, 0].detach().double(), edge @ w[:, 0].detach().double().abs()),
+                              ("w", got[1][:, 0], dh.T @ x[:, 0].detach().double(), edge.T @ x[:, 0].detach().double().abs()),
+                              ("b", got[2], dh.sum(0), e.sum(0))):
+        size = {"x": dh.abs() @ w[:, 0].detach().double().abs(), "w": dh.abs().T @ x[:, 0].detach().double().abs(),
+                "b": dh.abs().sum(0)}[name]
+        ok = ref.abs() <= most * (1 - 2 * u)
+        err = (a.double() - ref).abs() - (1.01 * tol + u * ref.abs() + (n + r) * 2.0 ** -24 * size + 2.0 ** -25)
+        assert a[ok].isfinite().all(), name
+        assert (err[ok] <= 0).all(), (name, float(err[ok].max()))
