@@ -152,7 +152,9 @@ LAPSUM_API int lapsum_experts_combine_bwd(const void* grad, int dtype, int64_t t
 #define LAPSUM_ACT_NONE 0
 #define LAPSUM_ACT_RELU 1
 #define LAPSUM_ACT_SILU 2
-#define LAPSUM_ACT_GELU 3     /* h Phi(h), Phi the normal CDF (by erf) */
+#define LAPSUM_ACT_GELU 3     /* h Phi(h), Phi the normal CDF (no tanh form); before
+                                 its rounding within 3e-6 of the value for |h| <= 4
+                                 and 2e-5 beyond, in the lower tail too */
 #define LAPSUM_ACT_SWIGLU 4   /* silu(h_i) h_{i + out/2}: half as wide */
 
 /* ---- asynchronous status bits of the products ----------------------------- */
@@ -179,8 +181,8 @@ LAPSUM_API int lapsum_experts_combine_bwd(const void* grad, int dtype, int64_t t
  *   residual    in   [rows, width] or NULL; width is out, or out/2 for
  *                    LAPSUM_ACT_SWIGLU
  *   y           out  [rows, width]
- *   preact      out  [rows, out] h = W_e x_r + b_e rounded to the type (what is
- *                    finite stays so, as the type's largest value; for
+ *   preact      out  [rows, out] h = W_e x_r + b_e rounded to the type (fp16: what
+ *                    is finite stays so, as the type's largest value; for
  *                    LAPSUM_ACT_RELU what is positive stays positive), which
  *                    the backward pass takes (rows from offsets[experts] on
  *                    are left as they were); or NULL.  y does not depend on it.

@@ -163,3 +163,34 @@ def test_gradients_where_a_pre_activation_leaves_the_type(dtype, act, r):
         err = (a.double() - ref).abs() - (1.01 * tol + u * ref.abs() + (n + r) * 2.0 ** -24 * size + 2.0 ** -25)
         assert a[ok].isfinite().all(), name
         assert (err[ok] <= 0).all(), (name, float(err[ok].max()))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_gelu_and_its_derivative_over_the_type(dtype):
+    """Every value of the type with 2^-100 <= |h| <= 13.5 (and 0): the error is relative, in the lower tail too."""
+    h = torch.arange(-2 ** 15, 2 ** 15, device="cuda").to(torch.int16).view(dtype)
+    d = h.double()
+    h = h[((d.abs() <= 13.5) & (d.abs() >= 2.0 ** -100)) | (d == 0)].contiguous()
+    d = h.double()
+    n = len(h)
+    cdf = 0.5 * torch.special.erfcx(d.abs() * 0.5 ** 0.5) * torch.exp(-0.5 * d * d)  # lower tail
+    cdf = torch.where(d < 0, cdf, 1.0 - cdf)
+    phi = torch.exp(-0.5 * d * d) / (2 * torch.pi) ** 0.5
+    # half a step of the type (in the range where its step is fixed, half of that); the exponential: two roundings of an
+    # argument of up to 132 in base 2 and its constant's, 3 * 132 * 2^-24 * log 2 = 1.6e-5, the tail's factor 1e-6, others 1e-6
+    u, rel = torch.finfo(dtype).eps / 2, 2e-5
+    least = torch.finfo(dtype).tiny * u + 2.0 ** -126
+    x, w = torch.zeros(n, 8, dtype=dtype, device="cuda"), torch.zeros(8, 8, dtype=dtype, device="cuda")
+    x[:, 0], w[:, 0] = h, 1.0
+    y = ex.linear(x, w, activation="gelu")
+    ref = d * cdf
+    err = (y[:, 3].double() - ref).abs() - ((u + rel) * ref.abs() + least)
+    assert (err <= 0).all(), (float(h[err.argmax()]), float(y[err.argmax(), 3]), float(ref[err.argmax()]))
+    pre, gy, gh = h[:, None].expand(n, 8).contiguous(), torch.ones(n, 8, dtype=dtype, device="cuda"), torch.empty(n, 8, dtype=dtype, device="cuda")
+    ex._call("linear_act_bwd", 0, gy.data_ptr(), 1 if dtype == BF16 else 2, n, 8, 8, pre.data_ptr(), 8, 1, None, 3, gh.data_ptr(), 8,
+             None, None, 0)
+    ref, size = cdf + d * phi, cdf + d.abs() * phi
+    # an exponential below 2^-126 counts as 0 (the code flushes subnormals): there the derivative is at most 2^-126 times
+    # 0.3990 |h| + 0.5 erfcx(|h| / sqrt 2) <= 0.3990 * 13.5 + 0.04 < 6 (|h| > 13.2)
+    err = (gh[:, 5].double() - ref).abs() - (u * ref.abs() + (1 + u) * rel * size + least + 5 * 2.0 ** -126)
+    assert (err <= 0).all(), (float(h[err.argmax()]), float(gh[err.argmax(), 5]), float(ref[err.argmax()]))
