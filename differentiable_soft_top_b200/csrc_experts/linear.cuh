@@ -318,33 +318,42 @@ __device__ __forceinline__ void finish(const Args& a, const Tile& t, int c0, int
         for (int i = 0; i < 16; ++i) v[h][i] += bias[2 * h + (i >> 1 & 1)];
     }
     if (a.preact) {
-      // what relu passes stays positive where it is kept (fp16 ends at 2^-24): its
-      // gradient asks for the sign.  Only there: y is the same whether it is kept or not
-      const bool sign = std::is_same<T, __half>::value && !kGated && a.activation == LAPSUM_ACT_RELU;
-      // and what is finite stays finite: y often is where h is not (silu of -7e4 in
-      // fp16), and an infinity would turn a gradient that vanishes into NaN
-      constexpr float most = std::is_same<T, __half>::value ? 65504.0f : 3.38953139e38f;
-      auto kept = [&](float x) {
-        if (sign && x > 0.0f) x = fmaxf(x, 6e-8f);
-        return fabsf(x) > most && fabsf(x) < INFINITY ? copysignf(most, x) : x;
-      };
-      if (kGated) {
+      // What fp16 cannot hold as it is: what relu passes stays positive (the type
+      // ends at 2^-24, and its gradient asks for the sign), and what is finite stays
+      // finite (y often is where h is not, as silu of -7e4, and an infinity would turn
+      // a gradient that vanishes into NaN).  In what is kept only: y does not change.
+      bool odd = false;
+      if constexpr (std::is_same<T, __half>::value) {
+        float big = 0.0f;
 #pragma unroll
-        for (int up = 0; up < 2; ++up) {
+        for (int i = 0; i < 16; ++i) big = fmaxf(big, fmaxf(fabsf(v[0][i]), fabsf(v[1][i])));
+        odd = __any_sync(0xffffffffu, big > 65504.0f) || (!kGated && a.activation == LAPSUM_ACT_RELU);
+      }
+      auto kept = [&](float x) {
+        if (!kGated && a.activation == LAPSUM_ACT_RELU && x > 0.0f) x = fmaxf(x, 6e-8f);
+        return fabsf(x) > 65504.0f && fabsf(x) < INFINITY ? copysignf(65504.0f, x) : x;
+      };
+#pragma unroll
+      for (int up = 0; up < (kGated ? 2 : 1); ++up) {
+        // gated: lane half g's gates or ups; else group g
+        auto pair = [&](int j, int g, auto as) {
+          const float(&from)[16] = v[kGated ? g : g >> 1];
+          const int at = 4 * j + 2 * (kGated ? up : g & 1);
+          f.p[j][g] = pack2<T>(as(from[at]), as(from[at + 1]));
+        };
+        if (odd) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) f.p[j][h] = pack2<T>(kept(v[h][4 * j + 2 * up]), kept(v[h][4 * j + 2 * up + 1]));
-          put<kGated>(f, base, static_cast<uint16_t*>(a.preact) + up * a.feat, row, a.preact_stride, feat0, a.feat, n, own,
-                      lane);
+            for (int g = 0; g < G; ++g) pair(j, g, kept);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int g = 0; g < G; ++g) pair(j, g, [](float x) { return x; });
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int g = 0; g < G; ++g)
-            f.p[j][g] = pack2<T>(kept(v[g >> 1][4 * j + 2 * (g & 1)]), kept(v[g >> 1][4 * j + 2 * (g & 1) + 1]));
-        put<kGated>(f, base, a.preact, row, a.preact_stride, feat0, a.feat, n, own, lane);
+        put<kGated>(f, base, static_cast<uint16_t*>(a.preact) + up * a.feat, row, a.preact_stride, feat0, a.feat, n, own,
+                    lane);
       }
     }
     if (kGated) {
