@@ -235,7 +235,9 @@ __device__ __forceinline__ bool keep_groups(const Rule& r, const Keys& in, const
         if (l[i] != -INFINITY) m = fmaxf(m, fabsf(l[i]));
       size = 4.0f * (warp_max(m) + in.bias_max);
     }
-    certain = hi == -INFINITY || lo - hi > scores + 2.4e-7f * size + 1e-37f;
+    // (a sum that left fp32's range looks like a group without experts, or like any other)
+    const bool whole = g >= r.groups || !first || fabsf((float)value) < INFINITY;
+    certain = __all_sync(kAll, whole) && (hi == -INFINITY || lo - hi > scores + 2.4e-7f * size + 1e-37f);
   }
   if (r.lanes) {
     if (!stays) {

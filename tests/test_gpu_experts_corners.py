@@ -6,7 +6,7 @@ pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="no CUDA device")]
 
 from differentiable_soft_top_b200 import experts as ex  # noqa: E402
-from tests.test_gpu_experts import route64, small_layer  # noqa: E402
+from tests.test_gpu_experts import INF, route64, small_layer  # noqa: E402
 
 F32, BF16, FP16 = torch.float32, torch.bfloat16, torch.float16
 
@@ -60,6 +60,37 @@ def test_route_near_ties_of_very_small_scores(score, top):
     b = torch.zeros(64, device="cuda")
     same_choice(x.cuda(), 8, score, b)
     same_choice(x.cuda(), 8, score, b, 8, 3, top)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("groups", [4, 3])
+@pytest.mark.parametrize("kept", [1, 2])
+def test_route_groups_whose_sum_leaves_fp32(dtype, groups, kept):
+    """Two keys of the lowest (or highest) value add up to more than fp32 holds: such a group still comes before one
+    without experts, and two such groups are told apart."""
+    low, most = torch.finfo(dtype).min, torch.finfo(dtype).max
+    x = torch.zeros(6, 24, device="cuda", dtype=dtype)
+    n = 24 // groups
+    x[0] = low
+    x[0, :n] = -INF                           # group 0 has nobody, the sums of the others are beyond fp32
+    x[1] = low
+    x[1, :n] = low / 2 * 1.5                  # all beyond, the first and the last higher
+    x[1, -n:] = low / 2 * 1.25
+    x[2] = most
+    x[2, -n:] = -INF
+    x[2, n:2 * n] = most / 2
+    x[3, :n] = most                           # +max and 0, a group of lows between
+    x[3, n:2 * n] = low
+    x[4] = low
+    x[4, 1::2] = -INF
+    x[4, :n] = -INF
+    x[5] = low
+    for bias in (None, torch.zeros(24, device="cuda"), torch.full((24,), torch.finfo(F32).min / 2, device="cuda")):
+        for top in (1, 2):
+            if bias is not None and bias.any():
+                same_choice(x[[0, 4, 5]], 3, "identity", bias, groups, kept, top)
+            else:
+                same_choice(x, 3, "identity", bias, groups, kept, top)
 
 
 # ---------------------------------------------------------------------------
