@@ -666,8 +666,12 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? 8 : kPer == 16 ? 6 : 3) 
       const float s = mine >= 0 ? load_score<kDtype>(a.scores, in.at + mine) : -INFINITY;
       if (a.renormalize) {
         if (a.score == LAPSUM_SCORE_IDENTITY) {
-          const float v = mine >= 0 ? s : 0.0f;
-          const float total = chosen_sum(v, a.k);
+          float v = mine >= 0 ? s : 0.0f;
+          float total = chosen_sum(v, a.k);
+          if (__any_sync(kAll, !(fabsf(total) < INFINITY))) {  // up to 32 values: 2^-8 of each stays in range
+            v *= 0.00390625f;
+            total = chosen_sum(v, a.k);
+          }
           w = total != 0.0f ? a.scale * (v / total) : 0.0f;
         } else {  // softmax over the chosen of log s: no sum can vanish
           const float v = a.score == LAPSUM_SCORE_SIGMOID && mine >= 0 ? log_sigmoid(s) : s;

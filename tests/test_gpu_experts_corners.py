@@ -93,6 +93,25 @@ def test_route_groups_whose_sum_leaves_fp32(dtype, groups, kept):
                 same_choice(x, 3, "identity", bias, groups, kept, top)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, FP16])
+@pytest.mark.parametrize("k", [2, 7, 32])
+def test_route_renormalised_memberships_of_the_highest_values(dtype, k):
+    """Weights are shares of a sum that fp32 need not hold."""
+    low, most = torch.finfo(dtype).min, torch.finfo(dtype).max
+    x = torch.zeros(5, 40, device="cuda", dtype=dtype)
+    x[0] = most
+    x[1] = low
+    x[2] = low                                # two scores, the places after them hold the lowest value
+    x[2, 5], x[2, 30] = 0.5, 0.25
+    x[3, ::3] = most / 2
+    x[4] = 0.5
+    w, e = ex.route(x, k, score="identity")
+    w0, e0 = route64(x, k, "identity", None, 1, 1, 1, True, 1.0)
+    assert torch.equal(e.cpu(), e0)
+    # a sum of k terms in a tree (5 roundings) and a quotient
+    torch.testing.assert_close(w.double().cpu(), w0, rtol=8 * 2.0 ** -24, atol=2.0 ** -126)
+
+
 # ---------------------------------------------------------------------------
 # autograd
 # ---------------------------------------------------------------------------
