@@ -353,6 +353,10 @@ __global__ void __launch_bounds__(kRowThreads)
     int row = __ldg(rows + s);
     if ((uint64_t)(int64_t)row >= (uint64_t)slots) row = -1;
     const float wt = weights ? __ldg(weights + s) : 1.0f;
+    // row number s has no slot: none in range, or one whose place was taken away
+    const int from = gy ? __ldg(slot_of + s) : 0;
+    const bool some = (uint64_t)(int64_t)from < (uint64_t)slots;
+    const int back = __ldg(rows + (some ? from : 0));
     float dot = 0.0f;
     if (row >= 0) {
       const P* gp = reinterpret_cast<const P*>(g + s / k * g_stride);
@@ -388,7 +392,7 @@ __global__ void __launch_bounds__(kRowThreads)
       for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
       if (lane == 0) gw[s] = dot;
     }
-    if (gy && __ldg(slot_of + s) < 0) {
+    if (gy && (!some || back != (int)s)) {
       P* op = reinterpret_cast<P*>(gy + s * gy_stride);
       for (int p = lane; p < packs; p += 32) op[p] = zero_pack<kDtype, kVec>();
     }

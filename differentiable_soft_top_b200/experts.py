@@ -288,7 +288,9 @@ def route(scores, k: int, *, score: str = "softmax", bias=None, groups: int = 1,
 
 @dataclass
 class Plan:
-    """Where the slots (token * k + j) of a choice stand in expert order."""
+    """Where the slots (token * k + j) of a choice stand in expert order: rows and
+    slots are each other's inverse.  A place may be taken away from combine()
+    by setting its row to -1."""
     offsets: object   # int32 [experts + 1]: expert e has rows offsets[e] .. offsets[e + 1] - 1
     rows: object      # int32 [tokens, k]: the row of a slot, -1 if its expert is -1
     slots: object     # int32 [tokens * k]: the slot of a row, -1 from offsets[-1] on

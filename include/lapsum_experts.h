@@ -141,7 +141,8 @@ LAPSUM_API int lapsum_experts_combine(const void* y, int dtype, int64_t tokens, 
  * Backward of lapsum_experts_combine for g = dL/dout [tokens, dim]:
  * grad_y[rows[t, j]] = w[t, j] g[t] (rows without a slot get 0) and
  * grad_weights[t, j] = <g[t], y[rows[t, j]]> (0 for a slot without a row).
- * Either output may be NULL.  slot_of is the plan's.
+ * Either output may be NULL.  slot_of is the plan's: the inverse of rows, of which
+ * places may have been taken away since (rows[t, j] = -1, the row then has no slot).
  */
 LAPSUM_API int lapsum_experts_combine_bwd(const void* grad, int dtype, int64_t tokens, int k, int64_t dim,
                                           int64_t grad_stride, const void* y, int64_t y_stride,

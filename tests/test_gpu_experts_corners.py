@@ -6,7 +6,7 @@ pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="no CUDA device")]
 
 from differentiable_soft_top_b200 import experts as ex  # noqa: E402
-from tests.test_gpu_experts import INF, route64, small_layer  # noqa: E402
+from tests.test_gpu_experts import INF, randn, route64, small_layer, some_choice  # noqa: E402
 
 F32, BF16, FP16 = torch.float32, torch.bfloat16, torch.float16
 
@@ -110,6 +110,39 @@ def test_route_renormalised_memberships_of_the_highest_values(dtype, k):
     assert torch.equal(e.cpu(), e0)
     # a sum of k terms in a tree (5 roundings) and a quotient
     torch.testing.assert_close(w.double().cpu(), w0, rtol=8 * 2.0 ** -24, atol=2.0 ** -126)
+
+
+# ---------------------------------------------------------------------------
+# exchange
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dim", [64, 7])
+def test_rows_without_a_slot_get_no_gradient(dim):
+    """Rows whose place was taken away after the plan was made, or whose slot is out of range, get 0, whatever stood
+    in the gradient's memory."""
+    t, k = 50, 3
+    c = some_choice(t, k, 8, seed=3)
+    p = ex.plan(c, 8)
+    taken = torch.rand(t, k, generator=torch.Generator().manual_seed(1)).cuda() < 0.3
+    p.rows[taken] = -1
+    y, w, g = randn(t * k, dim, seed=1), randn(t, k, seed=2).abs(), randn(t, dim, seed=3)
+    at = p.rows.long()
+    want = torch.zeros(t * k, dim, device="cuda")
+    want[at[at >= 0]] = (w[..., None] * g[:, None])[at >= 0]
+    gy, gw = torch.full_like(y, 7.0), torch.full_like(w, 7.0)
+    ex._call("combine_bwd", 0, g.data_ptr(), 0, t, k, dim, dim, y.data_ptr(), dim, w.data_ptr(), p.rows.data_ptr(),
+             p.slots.data_ptr(), gy.data_ptr(), dim, gw.data_ptr())
+    assert torch.equal(gy, want) and (gw[at < 0] == 0).all()
+    y.requires_grad_(), w.requires_grad_()
+    out = ex.combine(y, w, p)
+    dy, dw = torch.autograd.grad(out, [y, w], g)
+    assert torch.equal(dy, want) and torch.equal(dw, gw)
+    # slots out of range are none
+    rows = torch.tensor([[0, 9], [-3, 1]], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([0, 3, 77, -1], dtype=torch.int32, device="cuda")
+    gy = torch.full((4, dim), 7.0, device="cuda")
+    ex._call("combine_bwd", 0, g.data_ptr(), 0, 2, 2, dim, dim, y.data_ptr(), dim, None, rows.data_ptr(), slots.data_ptr(),
+             gy.data_ptr(), dim, None)
+    assert torch.equal(gy, torch.stack([g[0], g[1], g[0] * 0, g[0] * 0]))
 
 
 # ---------------------------------------------------------------------------
