@@ -472,7 +472,6 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated, kSplit>::kThreads, 
   volatile uint32_t* gave_up = tmem_at + 1;
   int* table = reinterpret_cast<int*>(tail + 512);
 
-  grid_launch_next();
   if (kSplit) cluster_arrive();  // waited for before the first access to another block's memory
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = kPair ? (int)cluster_rank() : 0;
@@ -491,7 +490,12 @@ __global__ void __launch_bounds__(Shape<kMode, kTok, kGated, kSplit>::kThreads, 
     mbar_init(drained, 1);
     *gave_up = 0u;
   }
-  if (warp == 1) tmem_alloc<kPair>(tmem_at, S::kTmemCols);
+  if (warp == 1) {
+    tmem_alloc<kPair>(tmem_at, S::kTmemCols);
+    // Not before: the next kernel may take tensor memory too, and this block's must
+    // not come behind that of a kernel which waits for this one's end.
+    grid_launch_next();
+  }
   grid_wait_previous();  // from here on the kernels before this one have finished
   if (kMode != kGradW) build_table<kTok>(a, table);
   tc_fence_before();
