@@ -68,11 +68,10 @@ constexpr int64_t kMaxIndex = INT32_MAX;
 
 // polls of a product's bounded waits (2^20: about a second), and the test knob
 constexpr uint32_t kPolls = 1u << 20;
-std::atomic<uint32_t> g_test_polls{0};
+thread_local uint32_t t_test_polls = 0;
 void set_limits(Product& p) {
-  const uint32_t test = g_test_polls.load(std::memory_order_relaxed);
-  p.polls = test ? test : kPolls;
-  p.starve = test != 0;
+  p.polls = t_test_polls ? t_test_polls : kPolls;
+  p.starve = t_test_polls != 0;
 }
 
 // A 16-bit matrix that tiled copies and 16-byte accesses reach: 16-byte rows.
@@ -102,7 +101,7 @@ extern "C" {
 
 const char* lapsum_experts_last_cuda_error(void) { return t_error; }
 
-void lapsum_experts_test_timeout(uint32_t polls) { g_test_polls.store(polls); }
+void lapsum_experts_test_timeout(uint32_t polls) { t_test_polls = polls; }
 
 static int route_args(const void* scores, int dtype, int64_t tokens, int experts, int64_t row_stride, int k, int score,
                       const float* bias, float scale) {

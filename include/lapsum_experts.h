@@ -273,8 +273,8 @@ LAPSUM_API int lapsum_experts_mlp_bwd(const void* grad, int dtype, int64_t token
                                       void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * Test knob, process-wide: with polls > 0 the products launched from now on
- * copy nothing and their waits give up after that many polls, so that they end
+ * Test knob of the calling host thread: with polls > 0 the products it launches
+ * from now on copy nothing and their waits give up after that many polls, so that they end
  * with LAPSUM_EXPERTS_TIMEOUT and NaN in every row that an expert owns (a weight
  * gradient: in every expert that has rows).  Nothing waits forever and no fault
  * is raised.  0: as usual again.

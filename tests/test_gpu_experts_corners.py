@@ -1,4 +1,6 @@
 """Corners of the expert operators' range against the definitions in 64 bits (B200)."""
+import threading
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -277,3 +279,20 @@ def test_gelu_and_its_derivative_over_the_type(dtype):
     # 0.3990 |h| + 0.5 erfcx(|h| / sqrt 2) <= 0.3990 * 13.5 + 0.04 < 6 (|h| > 13.2)
     err = (gh[:, 5].double() - ref).abs() - (u * ref.abs() + (1 + u) * rel * size + least + 5 * 2.0 ** -126)
     assert (err <= 0).all(), (float(h[err.argmax()]), float(gh[err.argmax(), 5]), float(ref[err.argmax()]))
+
+
+def test_the_test_knob_is_the_threads_own():
+    """While one host thread makes its products give up, those of another are right."""
+    x, w = randn(40, 64, seed=1, dtype=BF16), randn(128, 64, seed=2, dtype=BF16)
+    want, lib, got = ex.linear(x, w), ex._load(), []
+    lib.lapsum_experts_test_timeout(500)
+    try:
+        other = threading.Thread(target=lambda: got.append(ex.linear(x, w)))
+        other.start()
+        other.join()
+        own = ex.linear(x, w)
+        torch.cuda.synchronize()
+    finally:
+        lib.lapsum_experts_test_timeout(0)
+    assert torch.equal(got[0], want) and own.isnan().all()
+    assert torch.equal(ex.linear(x, w), want)
