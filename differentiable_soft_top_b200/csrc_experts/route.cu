@@ -12,7 +12,7 @@
 // Equal results whatever the rounding: fp32 keys, their last 5 bits replaced by
 // the place in the lane, decide only when neighbours in the order lie further
 // apart than that and the fp32 error can reach, or are truly equal.  Where they
-// do not (about 1 token in 50 at 256 sigmoid scores) the candidates are put in
+// do not (about 1 token in 60 at 256 sigmoid scores) the candidates are put in
 // order by fp64 keys; where that does not settle it, all experts are.  Without a
 // bias and without sums of two keys the order of the keys is the order of the
 // scores, which 16-bit scores show exactly.
@@ -522,10 +522,7 @@ __device__ __noinline__ uint32_t groups_again(Rule r, Keys in) {
   load_biases<kPer>(in.bias, r.experts, false, b);
   mask_token<true>(l, b);
   uint64_t o[kPer];
-  if (r.raw)
-    keys_of<double, true>(r, in, l, b, o);
-  else
-    keys_of<double, false>(r, in, l, b, o);
+  keys_of<double, false>(r, in, l, b, o);
   keep_groups<double, false>(r, in, l, o);
   uint32_t stay = 0;
 #pragma unroll
@@ -541,7 +538,7 @@ template <int kDtype, int kPer>
 __device__ __noinline__ bool order_again(Rule r, Keys in, int* picked, int count) {
   const int lane = threadIdx.x & 31;
   double total = 1.0;
-  if (!r.raw && r.score == LAPSUM_SCORE_SOFTMAX) {
+  if (r.score == LAPSUM_SCORE_SOFTMAX) {
     float l[kPer], b[kPer];
     load_token<kDtype, kPer>(in.scores, in.at, r.experts, false, l);
     load_biases<kPer>(in.bias, r.experts, false, b);
@@ -557,10 +554,8 @@ __device__ __noinline__ bool order_again(Rule r, Keys in, int* picked, int count
   double key = -INFINITY, s = 0.0;
   if (e >= 0) {
     s = (double)load_score<kDtype>(in.scores, in.at + e);
-    if (!r.raw) {
-      if (r.score == LAPSUM_SCORE_SOFTMAX) s = exp(s - (double)in.top) * (1.0 / total);
-      if (r.score == LAPSUM_SCORE_SIGMOID) s = 1.0 / (1.0 + exp(-s));
-    }
+    if (r.score == LAPSUM_SCORE_SOFTMAX) s = exp(s - (double)in.top) * (1.0 / total);
+    if (r.score == LAPSUM_SCORE_SIGMOID) s = 1.0 / (1.0 + exp(-s));
     key = s + (in.bias ? (double)__ldg(in.bias + e) : 0.0);
   }
   int rank = 0;
