@@ -74,6 +74,17 @@ __device__ __forceinline__ float key_of(uint32_t o) {
 __device__ __forceinline__ double key_of(uint64_t o) {
   return __longlong_as_double((int64_t)(o >> 63 ? o ^ 0x8000000000000000ull : ~o));
 }
+// with its subnormal values, which the code's conversions flush
+__device__ __forceinline__ double wide(float f) {
+  double d;
+  asm("cvt.f64.f32 %0, %1;" : "=d"(d) : "f"(f));
+  return d;
+}
+template <typename K>
+__device__ __forceinline__ K as_key(float f) {
+  if constexpr (sizeof(K) == 8) return wide(f);
+  else return f;
+}
 __device__ __forceinline__ uint32_t warp_top(uint32_t v) { return __reduce_max_sync(kAll, v); }
 __device__ __forceinline__ uint64_t warp_top(uint64_t v) {
   const uint32_t hi = __reduce_max_sync(kAll, (uint32_t)(v >> 32));
@@ -91,7 +102,6 @@ struct Rule {
   int experts, k, score;
   int groups, size, kept, top;  // size: experts of a group
   int lanes;                    // of a group: a power of two, or 0 (groups are not whole lanes)
-  bool raw;                     // the scores themselves are in the order of the keys
 };
 
 template <typename K>
@@ -120,6 +130,14 @@ __device__ __forceinline__ void top_two(O& a, O& b, O c, O d) {
   a = max(a, c);
 }
 template <typename O>
+__device__ __forceinline__ O shuffle(O v, int from) {
+  return (O)__shfl_sync(kAll, (unsigned long long)v, from);
+}
+template <>
+__device__ __forceinline__ uint32_t shuffle<uint32_t>(uint32_t v, int from) {
+  return __shfl_sync(kAll, v, from);
+}
+template <typename O>
 __device__ __forceinline__ O shuffle_xor(O v, int d) {
   return (O)__shfl_xor_sync(kAll, (unsigned long long)v, d);
 }
@@ -128,10 +146,11 @@ __device__ __forceinline__ uint32_t shuffle_xor<uint32_t>(uint32_t v, int d) {
   return __shfl_xor_sync(kAll, v, d);
 }
 
-template <typename K>
-__device__ __forceinline__ typename Order<K>::O raw_base() {
-  return ordered((K)-INFINITY) - 31u;
-}
+// kRaw: the scores themselves are in the order of the keys.  They are compared as
+// integers throughout (fp32's subnormal values would be flushed), counted from the
+// integer of -inf, so that the lowest finite score has 32: what is below stands for
+// nothing once the last 5 bits are replaced.
+constexpr uint32_t kRawBase = 0x007fffffu - 31u;
 
 // o: the ordered keys of this lane's experts (0: not there)
 template <typename K, bool kRaw, int kPer>
@@ -139,27 +158,25 @@ __device__ __forceinline__ void keys_of(const Rule& r, const Keys& in, const flo
                                         typename Order<K>::O (&o)[kPer]) {
   using O = typename Order<K>::O;
   if (kRaw) {
-    // counted from the key of -inf, so that the lowest finite score has 32 (what
-    // is below stands for nothing once the last 5 bits are replaced)
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = l[i] == -INFINITY ? O(0) : ordered((K)l[i]) - raw_base<K>();
+    for (int i = 0; i < kPer; ++i) o[i] = l[i] == -INFINITY ? O(0) : O(ordered(l[i]) - kRawBase);
     return;
   }
-  const K top = (K)in.top;
+  const K top = as_key<K>(in.top);
   K scale = (K)in.scale;
   if (sizeof(K) == 8 && r.score == LAPSUM_SCORE_SOFTMAX) {
     K s = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (l[i] != -INFINITY) s += exp_of((K)l[i] - top);
+      if (l[i] != -INFINITY) s += exp_of(as_key<K>(l[i]) - top);
     scale = quotient((K)1, warp_sum(s));
   }
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    K s = (K)l[i];
+    K s = as_key<K>(l[i]);
     if (r.score == LAPSUM_SCORE_SOFTMAX) s = exp_of(s - top) * scale;
     if (r.score == LAPSUM_SCORE_SIGMOID) s = quotient((K)1, (K)1 + exp_of(-s));
-    o[i] = l[i] == -INFINITY ? O(0) : ordered(s + (K)b[i]);
+    o[i] = l[i] == -INFINITY ? O(0) : ordered(s + as_key<K>(b[i]));
   }
 }
 
@@ -174,7 +191,7 @@ __device__ __forceinline__ float score_error(float s) {
 
 // Clears the keys of the groups that go.  Returns whether the lowest value that
 // stays and the highest that goes are apart by more than fp32's error (kCheck).
-template <typename K, bool kCheck, int kPer>
+template <typename K, bool kCheck, bool kRaw, int kPer>
 __device__ __forceinline__ bool keep_groups(const Rule& r, const Keys& in, const float (&l)[kPer],
                                             typename Order<K>::O (&o)[kPer]) {
   using O = typename Order<K>::O;
@@ -209,18 +226,25 @@ __device__ __forceinline__ bool keep_groups(const Rule& r, const Keys& in, const
       }
     }
   }
-  const O from = r.raw ? raw_base<K>() : O(0);
-  K value = first ? key_of(first + from) : (K)-INFINITY;
-  if (r.top == 2 && second) value += key_of(second + from);
-  if (g >= r.groups) value = -INFINITY;
   int above = 0;
-  for (int q = 0; q < r.groups; ++q) {
-    const K v = __shfl_sync(kAll, value, q * lanes);
-    above += (v > value || (v == value && q < g)) ? 1 : 0;
+  K value = -INFINITY;
+  if constexpr (kRaw) {  // one key of a group counts
+    for (int q = 0; q < r.groups; ++q) {
+      const O v = shuffle(first, q * lanes);
+      above += (v > first || (v == first && q < g)) ? 1 : 0;
+    }
+  } else {
+    if (first) value = key_of(first);
+    if (r.top == 2 && second) value += key_of(second);
+    if (g >= r.groups) value = -INFINITY;
+    for (int q = 0; q < r.groups; ++q) {
+      const K v = __shfl_sync(kAll, value, q * lanes);
+      above += (v > value || (v == value && q < g)) ? 1 : 0;
+    }
   }
   const bool stays = g < r.groups && above < r.kept;
   bool certain = true;
-  if (kCheck && !r.raw) {
+  if constexpr (kCheck) {
     // a value is the sum of up to two keys, each off by its score's error and
     // 2^-24 of itself, and scores are at most a key plus the largest bias
     const float lo = -warp_max(stays ? -(float)value : -INFINITY);
@@ -289,7 +313,7 @@ __device__ __forceinline__ bool choose(const Rule& r, const Keys& in, const floa
   keys_of<float, kRaw>(r, in, l, b, o);
   bool certain = true;
   if (r.kept < r.groups) {
-    const bool sure = keep_groups<float, !kRaw>(r, in, l, o);
+    const bool sure = keep_groups<float, !kRaw, kRaw>(r, in, l, o);
     if constexpr (!kRaw)
       if (!sure) {
         const uint32_t stay = groups_again<kDtype, kPer>(r, in);
@@ -333,15 +357,14 @@ __device__ __forceinline__ bool choose(const Rule& r, const Keys& in, const floa
     const int e1 = mine >= 0 ? picked[lane + 1] : -1;
     if (e1 >= 0) {
       const float score = load_score<kDtype>(in.scores, in.at + mine), score1 = load_score<kDtype>(in.scores, in.at + e1);
-      float key = score, key1 = score1, bound = 0.0f;
-      bool same = score == score1;
-      if (!kRaw) {
+      if constexpr (kRaw) {
+        const uint32_t place = ordered(score), place1 = ordered(score1);
+        certain = lane == r.k - 1 ? (place & ~31u) > (place1 & ~31u) : place >= place1;
+      } else {
         const float bias = in.bias ? __ldg(in.bias + mine) : 0.0f, bias1 = in.bias ? __ldg(in.bias + e1) : 0.0f;
-        same = same && bias == bias1;
-        if (r.score == LAPSUM_SCORE_IDENTITY) {
-          key = score + bias;
-          key1 = score1 + bias1;
-        } else {
+        const bool same = ordered(score) == ordered(score1) && ordered(bias) == ordered(bias1) && lane != r.k - 1;
+        float key = score + bias, key1 = score1 + bias1, bound = 0.0f;
+        if (r.score != LAPSUM_SCORE_IDENTITY) {
           float s, s1;
           if (r.score == LAPSUM_SCORE_SIGMOID) {
             s = quotient(1.0f, 1.0f + exp_of(-score));
@@ -358,12 +381,9 @@ __device__ __forceinline__ bool choose(const Rule& r, const Keys& in, const floa
           bound = score_error(s) + score_error(s1);
         }
         bound += 2.4e-7f * (fabsf(key) + fabsf(key1)) + 1e-37f;  // the last: flushed subnormals
+        if (lane == r.k - 1) bound += 4e-6f * fabsf(key1);
+        certain = key - key1 > bound || same;
       }
-      if (lane == r.k - 1) {
-        bound += 4e-6f * fabsf(key1) + 1e-37f;
-        same = false;
-      }
-      if (!(key - key1 > bound) && !same) certain = false;
     }
     certain = __all_sync(kAll, certain);
     if (!kRaw && !certain && r.k + 2 <= 32) {  // put the candidates and one more in order by their fp64 keys
@@ -377,17 +397,14 @@ __device__ __forceinline__ bool choose(const Rule& r, const Keys& in, const floa
   return certain;
 }
 
-// The same with fp64 keys, none of whose bits is replaced.
-template <int kPer>
+// The same with fp64 keys (kRaw: the scores' integers), none of whose bits is replaced.
+template <bool kRaw, int kPer>
 __device__ __forceinline__ int choose_exact(const Rule& r, const Keys& in, const float (&l)[kPer], const float (&b)[kPer],
                                             int* picked) {
   const int lane = threadIdx.x & 31;
   uint64_t o[kPer];
-  if (r.raw)
-    keys_of<double, true>(r, in, l, b, o);
-  else
-    keys_of<double, false>(r, in, l, b, o);
-  if (r.kept < r.groups) keep_groups<double, false>(r, in, l, o);
+  keys_of<double, kRaw>(r, in, l, b, o);
+  if (r.kept < r.groups) keep_groups<double, false, kRaw>(r, in, l, o);
   for (int j = lane; j < r.k; j += 32) picked[j] = -1;
   __syncwarp();
   for (int j = 0; j < r.k; ++j) {
@@ -523,7 +540,7 @@ __device__ __noinline__ uint32_t groups_again(Rule r, Keys in) {
   mask_token<true>(l, b);
   uint64_t o[kPer];
   keys_of<double, false>(r, in, l, b, o);
-  keep_groups<double, false>(r, in, l, o);
+  keep_groups<double, false, false>(r, in, l, o);
   uint32_t stay = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) stay |= o[i] ? 1u << i : 0u;
@@ -546,17 +563,17 @@ __device__ __noinline__ bool order_again(Rule r, Keys in, int* picked, int count
     total = 0.0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (l[i] != -INFINITY) total += exp((double)l[i] - (double)in.top);
+      if (l[i] != -INFINITY) total += exp(wide(l[i]) - wide(in.top));
     total = warp_sum(total);
   }
   int e = lane < count ? picked[lane] : -1;
   count = __popc(__ballot_sync(kAll, e >= 0));
   double key = -INFINITY, s = 0.0;
   if (e >= 0) {
-    s = (double)load_score<kDtype>(in.scores, in.at + e);
-    if (r.score == LAPSUM_SCORE_SOFTMAX) s = exp(s - (double)in.top) * (1.0 / total);
+    s = wide(load_score<kDtype>(in.scores, in.at + e));
+    if (r.score == LAPSUM_SCORE_SOFTMAX) s = exp(s - wide(in.top)) * (1.0 / total);
     if (r.score == LAPSUM_SCORE_SIGMOID) s = 1.0 / (1.0 + exp(-s));
-    key = s + (in.bias ? (double)__ldg(in.bias + e) : 0.0);
+    key = s + (in.bias ? wide(__ldg(in.bias + e)) : 0.0);
   }
   int rank = 0;
   for (int j = 0; j < count; ++j) {
@@ -582,13 +599,13 @@ __device__ __noinline__ bool order_again(Rule r, Keys in, int* picked, int count
 }
 
 // The choice of a token whose fp32 keys lie too close.
-template <int kDtype, int kPer>
+template <int kDtype, int kPer, bool kRaw>
 __device__ __noinline__ int choose_again(Rule r, Keys in, int* picked) {
   float l[kPer], b[kPer];
   load_token<kDtype, kPer>(in.scores, in.at, r.experts, false, l);
   load_biases<kPer>(in.bias, r.experts, false, b);
   mask_token<true>(l, b);
-  return choose_exact<kPer>(r, in, l, b, picked);
+  return choose_exact<kRaw>(r, in, l, b, picked);
 }
 
 // sums and maxima over the k lanes that hold a choice (the others: neutral)
@@ -619,9 +636,8 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? 8 : kPer == 16 ? 6 : 3) 
   r.size = a.experts / a.groups;
   r.kept = a.groups_kept;
   r.top = a.group_top;
-  r.raw = kRaw;
   r.lanes = r.size % kPer == 0 && ((r.size / kPer) & (r.size / kPer - 1)) == 0 ? r.size / kPer : 0;
-  const bool soft = a.score == LAPSUM_SCORE_SOFTMAX && (!r.raw || !a.renormalize);
+  const bool soft = a.score == LAPSUM_SCORE_SOFTMAX && (!kRaw || !a.renormalize);
   // the sum of softmax scores whose order is that of the scores holds the largest
   const bool check_sum = a.score == LAPSUM_SCORE_SIGMOID || soft;
   const int64_t step = (int64_t)gridDim.x * kWarps;
@@ -657,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? 8 : kPer == 16 ? 6 : 3) 
           if (l[i] != -INFINITY) total += __expf(l[i] - in.top);
         in.scale = 1.0f / warp_sum(total);
       }
-      if (!choose<kDtype, kPer, kRaw>(r, in, l, b, picked, mine)) mine = choose_again<kDtype, kPer>(r, in, picked);
+      if (!choose<kDtype, kPer, kRaw>(r, in, l, b, picked, mine)) mine = choose_again<kDtype, kPer, kRaw>(r, in, picked);
       const float s = mine >= 0 ? load_score<kDtype>(a.scores, in.at + mine) : -INFINITY;
       if (a.renormalize) {
         if (a.score == LAPSUM_SCORE_IDENTITY) {

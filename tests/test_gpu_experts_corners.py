@@ -95,6 +95,21 @@ def test_route_groups_whose_sum_leaves_fp32(dtype, groups, kept):
                 same_choice(x, 3, "identity", bias, groups, kept, top)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("e,k,groups,kept", [(40, 6, 1, 1), (40, 6, 4, 2), (300, 32, 1, 1), (33, 5, 3, 2)])
+def test_route_subnormal_memberships(dtype, e, k, groups, kept):
+    """Memberships below 2^-126, as a sharp soft choice gives to all but a few experts, are told apart."""
+    g = torch.Generator().manual_seed(e)
+    x = torch.rand(60, e, generator=g, dtype=torch.float64) * 1e-39
+    x[:, ::7] *= -1.0
+    x[::4, 3] = 0.25
+    x = x.to(dtype).cuda()
+    b = (torch.randn(e, generator=g, dtype=torch.float64) * 1e-39).float().cuda()
+    for bias in (None, b):
+        for top in (1, 2):
+            same_choice(x, k, "identity", bias, groups, kept, top)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16, FP16])
 @pytest.mark.parametrize("k", [2, 7, 32])
 def test_route_renormalised_memberships_of_the_highest_values(dtype, k):
