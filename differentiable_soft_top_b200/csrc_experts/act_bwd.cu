@@ -4,8 +4,11 @@
 // A tile is 64 rows of one expert by 256 columns; 8 row lanes of a block each
 // add up their rows in registers, join in shared memory and leave one fp32
 // partial per tile and column, which a second kernel adds in the order of the
-// tiles (no atomics: the same bits every time).  Bound by memory: dY and H in,
-// dH out; the partials are 1/64 of that.
+// tiles (no atomics: the same bits every time).  dH is rounded to the type, in
+// which the two products that follow take it; the bias sums add it unrounded.  Bound
+// by memory: dY and H in, dH out; the partials are 1/64 of that.  Measured at 16384
+// x 4096, bf16, in a graph: relu 67 us (6.0 TB/s), silu 73, gelu 78, swiglu (2 x
+// 2048) 54 (6.2); the bias sums add 10 to 12.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

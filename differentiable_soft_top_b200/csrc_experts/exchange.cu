@@ -4,9 +4,11 @@
 //
 // All but the plan are bound by memory: 16 bytes per lane and access where the
 // addresses allow it, 8 accesses of a lane in flight.  Measured at 4096 tokens x
-// 8 x 2048, bf16: dispatch 29 us (5.2 TB/s), weighted sum 37 (4.1), its gradient
-// 48 (5.9); plan of those 32768 slots 9.  Short batches split a row over several
-// warps so that the GPU is full.
+// 8 x 2048, bf16, in a graph, inputs larger than L2: dispatch 29 us (5.3 TB/s),
+// weighted sum 31 (4.9), with a residual 37 (4.6), its gradient 47 (6.1); plan of
+// those 32768 slots 8.  For short batches dispatch splits a row over several warps
+// so that the GPU is full; the weighted sum has at most a block per token, its
+// gradient a warp per slot.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -268,7 +270,8 @@ __global__ void __launch_bounds__(kRowThreads) k_dispatch(const typename Elem<kD
 // as long as the block allows: DRAM likes 4 KB of a row at once (a warp per
 // token, which came back for 512 bytes of each row at a time, took 1.3 to 2
 // times as long).  The next token's row numbers are read ahead; the grid is what
-// is resident (8 blocks per SM of work in turn: 43 us, 2: 41, 4096 x 8 x 2048).
+// is resident (8 blocks per SM of work in turn: 43 us, 2: 41, 4096 x 8 x 2048 with
+// a residual, between events).
 template <int kDtype, int kVec, int kRows, int kPacks>
 __global__ void __launch_bounds__(kRowThreads, 2)
     k_combine(const typename Elem<kDtype>::T* __restrict__ y, int64_t y_stride, const float* __restrict__ weights,

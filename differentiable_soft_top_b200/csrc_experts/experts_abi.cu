@@ -460,7 +460,11 @@ int lapsum_experts_linear_bwd(const void* grad_y, int dtype, int64_t rows, int64
 }
 
 // Workspace of the layer: the plan's arrays and scratch, then the rows before,
-// between and after the products, each on a 256-byte boundary.
+// between and after the products, each on a 256-byte boundary.  The rows are of the
+// type: those between the products are the second one's operand, which the tensor
+// cores take in 16 bits; those after it (and the pre-activation that is kept) could
+// be fp32, for twice the bytes of the layer's largest arrays: a rounding each, half a
+// step of the type, as where the products are called one by one.
 struct MlpLayout {
   size_t offsets, rows, slots, plan, x_rows, pre, h, y, total;
   int64_t hidden;
@@ -560,7 +564,9 @@ int lapsum_experts_mlp_fwd(const void* x, int dtype, int64_t tokens, int64_t dim
   return rc;
 }
 
-// Scratch of the layer's backward: the rows' gradients and the products' own.
+// Scratch of the layer's backward: the rows' gradients and the products' own.  They
+// are of the type: gy and gh are operands of the products, gx (which combine adds up
+// in fp32) would be twice the bytes in fp32.
 struct MlpBwdLayout {
   size_t gy, gh, gx, products, total;
 };
