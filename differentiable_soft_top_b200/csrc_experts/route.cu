@@ -113,8 +113,8 @@ struct Order<double> {
   using O = uint64_t;
 };
 
-// What the order of a token's keys rests on; the fp32 bounds need the largest
-// bias (in magnitude, of the experts that are not masked).
+// What the order of a token's keys rests on; the fp32 bounds of the groups need the
+// largest bias.
 struct Keys {
   const void* scores;
   int64_t at;         // the token's first score
@@ -282,7 +282,7 @@ __device__ __forceinline__ bool keep_groups(const Rule& r, const Keys& in, const
 template <int kDtype, int kPer>
 __device__ __noinline__ uint32_t groups_again(Rule r, Keys in);
 template <int kDtype, int kPer>
-__device__ __noinline__ bool order_again(Rule r, Keys in, int* picked, int count);
+__device__ __noinline__ bool order_again(Rule r, Keys in, int* picked, int count, bool sure);
 
 // o in descending order (Batcher's odd-even merge sort)
 template <int N>
@@ -355,6 +355,8 @@ __device__ __forceinline__ bool choose(const Rule& r, const Keys& in, const floa
     // neighbours in the order: apart by more than their errors, or truly equal;
     // the last place also by more than the bits that were replaced (2^-18)
     const int e1 = mine >= 0 ? picked[lane + 1] : -1;
+    bool far = true;
+    float others = 0.0f;
     if (e1 >= 0) {
       const float score = load_score<kDtype>(in.scores, in.at + mine), score1 = load_score<kDtype>(in.scores, in.at + e1);
       if constexpr (kRaw) {
@@ -375,22 +377,30 @@ __device__ __forceinline__ bool choose(const Rule& r, const Keys& in, const floa
           }
           key = s + bias;
           key1 = s1 + bias1;
-          // what was not picked has no higher key than key1, but its score may be
-          // larger, and its error with it: its bias may take nearly all of it away
-          if (lane == r.k - 1) s1 = fmaxf(s1, key1 + in.bias_max);
           bound = score_error(s) + score_error(s1);
+          // What was not picked has no higher key than key1, but its score may be as
+          // large as 1, and its error with it: its bias may take nearly all of it away.
+          if (lane == r.k - 1 && in.bias) others = score_error(1.0f);
         }
         bound += 2.4e-7f * (fabsf(key) + fabsf(key1)) + 1e-37f;  // the last: flushed subnormals
         if (lane == r.k - 1) bound += 4e-6f * fabsf(key1);
         certain = key - key1 > bound || same;
+        far = same || key - key1 > bound + others;
       }
     }
-    certain = __all_sync(kAll, certain);
-    if (!kRaw && !certain && r.k + 2 <= 32) {  // put the candidates and one more in order by their fp64 keys
-      const int count = more && pick(r.k + 1) ? r.k + 2 : r.k + 1;
-      __syncwarp();
-      certain = order_again<kDtype, kPer>(r, in, picked, count);
-      mine = lane < r.k ? picked[lane] : -1;
+    if constexpr (kRaw) {
+      certain = __all_sync(kAll, certain);
+    } else {
+      const bool all_far = __all_sync(kAll, far);
+      if (!all_far && r.k + 2 <= 32) {  // put the candidates and one more in order by their fp64 keys
+        const bool sure = __all_sync(kAll, certain);
+        const int count = more && pick(r.k + 1) ? r.k + 2 : r.k + 1;
+        __syncwarp();
+        certain = order_again<kDtype, kPer>(r, in, picked, count, sure);
+        mine = lane < r.k ? picked[lane] : -1;
+      } else {
+        certain = all_far;
+      }
     }
   }
   __syncwarp();
@@ -524,6 +534,16 @@ __device__ __forceinline__ bool mask_token(float (&l)[kPer], const float (&b)[kP
   return __all_sync(kAll, fine);
 }
 
+// The largest bias in magnitude of the experts that are not masked
+template <int kPer>
+__device__ __forceinline__ float largest_bias(const float (&l)[kPer], const float (&b)[kPer]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (l[i] != -INFINITY) m = fmaxf(m, fabsf(b[i]));
+  return __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(m)));  // of values >= 0
+}
+
 // This lane's scores of the token, padding -inf
 template <int kDtype, int kPer>
 __device__ __forceinline__ void load_token(const void* scores, int64_t at, int experts, bool vec, float (&l)[kPer]) {
@@ -550,21 +570,45 @@ __device__ __noinline__ uint32_t groups_again(Rule r, Keys in) {
 // Puts the count candidates in picked[] (the highest fp32 keys, at most 32) in
 // the order of their fp64 keys.  False when an expert that is not among them
 // could belong to the first k: the last candidate, above whose fp32 key none of
-// the others lies, is too near the k-th.
+// the others lies, is too near the k-th.  sure: the candidates themselves are in
+// order as they are.
 template <int kDtype, int kPer>
-__device__ __noinline__ bool order_again(Rule r, Keys in, int* picked, int count) {
+__device__ __noinline__ bool order_again(Rule r, Keys in, int* picked, int count, bool sure) {
   const int lane = threadIdx.x & 31;
   double total = 1.0;
-  if (r.score == LAPSUM_SCORE_SOFTMAX) {
+  float bias_max = 0.0f;
+  if (r.score != LAPSUM_SCORE_IDENTITY) {
     float l[kPer], b[kPer];
     load_token<kDtype, kPer>(in.scores, in.at, r.experts, false, l);
     load_biases<kPer>(in.bias, r.experts, false, b);
     mask_token<true>(l, b);
-    total = 0.0;
+    auto key_error = [&](float x, float bias, float& key) {
+      const float s = r.score == LAPSUM_SCORE_SIGMOID ? quotient(1.0f, 1.0f + exp_of(-x)) : exp_of(x - in.top) * in.scale;
+      key = s + bias;
+      return score_error(s) + 2.4e-7f * fabsf(key) + 1e-37f;
+    };
+    if (sure && r.kept == r.groups) {
+      // as things are, if no more than k experts reach the k-th key, each with its own error
+      const int kth = picked[r.k - 1];
+      float low;
+      const float error = key_error(load_score<kDtype>(in.scores, in.at + kth), in.bias ? __ldg(in.bias + kth) : 0.0f, low);
+      int reach = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (l[i] != -INFINITY) total += exp(wide(l[i]) - wide(in.top));
-    total = warp_sum(total);
+      for (int i = 0; i < kPer; ++i) {
+        float key;
+        const float up = key_error(l[i], b[i], key);
+        reach += __popc(__ballot_sync(kAll, l[i] != -INFINITY && !(key + up < low - error)));
+      }
+      if (reach == r.k) return true;
+    }
+    bias_max = largest_bias(l, b);
+    if (r.score == LAPSUM_SCORE_SOFTMAX) {
+      total = 0.0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (l[i] != -INFINITY) total += exp(wide(l[i]) - wide(in.top));
+      total = warp_sum(total);
+    }
   }
   int e = lane < count ? picked[lane] : -1;
   count = __popc(__ballot_sync(kAll, e >= 0));
@@ -586,10 +630,11 @@ __device__ __noinline__ bool order_again(Rule r, Keys in, int* picked, int count
     const int kth = __ffs(__ballot_sync(kAll, e >= 0 && rank == r.k - 1)) - 1;
     const double low = __shfl_sync(kAll, key, kth);
     const double last = __shfl_sync(kAll, key, count - 1), last_s = __shfl_sync(kAll, s, count - 1);
-    // (those others may have larger scores than the last candidate, as in choose)
+    // (those others may have larger scores than the last candidate, as in choose, but
+    // none above its key and the largest bias)
     float error = 0.0f;
     if (r.score != LAPSUM_SCORE_IDENTITY)
-      error = score_error((float)last_s) + score_error((float)fmax(last_s, last + (double)in.bias_max));
+      error = score_error((float)last_s) + score_error((float)fmax(last_s, last + (double)bias_max));
     certain = low - last > 1e-5 * fabs(last) + (double)error + 1e-37;
   }
   __syncwarp();
@@ -656,12 +701,7 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? 8 : kPer == 16 ? 6 : 3) 
     float w = 0.0f;
     if (fine) {
       float m = 0.0f;
-      if (!kRaw && a.bias) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (l[i] != -INFINITY) m = fmaxf(m, fabsf(b[i]));
-        m = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(m)));  // of values >= 0
-      }
+      if (!kRaw && r.kept < r.groups && a.bias) m = largest_bias(l, b);
       in.bias_max = m;
       if (soft) {
         float top = -INFINITY, total = 0.0f;
@@ -677,11 +717,13 @@ __global__ void __launch_bounds__(kThreads, kPer <= 8 ? 8 : kPer == 16 ? 6 : 3) 
       const float s = mine >= 0 ? load_score<kDtype>(a.scores, in.at + mine) : -INFINITY;
       if (a.renormalize) {
         if (a.score == LAPSUM_SCORE_IDENTITY) {
+          // (where the sum leaves fp32's range, of 2^-8 of the up to 32 values)
           float v = mine >= 0 ? s : 0.0f;
           float total = chosen_sum(v, a.k);
-          if (__any_sync(kAll, !(fabsf(total) < INFINITY))) {  // up to 32 values: 2^-8 of each stays in range
+          const float small = chosen_sum(v * 0.00390625f, a.k);
+          if (!(fabsf(total) < INFINITY)) {
             v *= 0.00390625f;
-            total = chosen_sum(v, a.k);
+            total = small;
           }
           w = total != 0.0f ? a.scale * (v / total) : 0.0f;
         } else {  // softmax over the chosen of log s: no sum can vanish
