@@ -296,6 +296,22 @@ def test_gelu_and_its_derivative_over_the_type(dtype):
     assert (err <= 0).all(), (float(h[err.argmax()]), float(gh[err.argmax(), 5]), float(ref[err.argmax()]))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_gelu_at_infinity_and_nan(dtype):
+    """The limits of gelu at infinite pre-activations, NaN where they are NaN, and its derivative at the ends of what is
+    finite."""
+    h = torch.tensor([INF, -INF, float("nan"), torch.finfo(dtype).max, torch.finfo(dtype).min, 0.0, -0.0, 1.0], device="cuda").to(dtype)
+    x, w = torch.zeros(8, 8, dtype=dtype, device="cuda"), torch.zeros(8, 8, dtype=dtype, device="cuda")
+    b = h.clone()  # by the bias, so that no infinity meets another input's 0
+    y = ex.linear(x, w, bias=b, activation="gelu")[0]
+    assert y[0] == INF and y[1] == 0 and y[2].isnan() and y[3] == torch.finfo(dtype).max and (y[4:7] == 0).all()
+    pre, gy, gh = h[:, None].expand(8, 8).contiguous(), torch.ones(8, 8, dtype=dtype, device="cuda"), torch.empty(8, 8, dtype=dtype, device="cuda")
+    ex._call("linear_act_bwd", 0, gy.data_ptr(), 1 if dtype == BF16 else 2, 8, 8, 8, pre.data_ptr(), 8, 1, None, 3, gh.data_ptr(), 8,
+             None, None, 0)
+    d = gh[:, 0].tolist()
+    assert d[2] != d[2] and d[3:7] == [1.0, 0.0, 0.5, 0.5]
+
+
 def test_the_test_knob_is_the_threads_own():
     """While one host thread makes its products give up, those of another are right."""
     x, w = randn(40, 64, seed=1, dtype=BF16), randn(128, 64, seed=2, dtype=BF16)
