@@ -6,14 +6,16 @@
 // of two of them, find their two highest keys in log2 steps, all groups at
 // once.  The floor is the scores' bytes; what bounds it is the issue of integer
 // instructions (the ALU pipe), some 30 for each of the k rounds.  Measured at
-// 16384 x 256, k = 8: bf16 scores 12 us, fp32 17, sigmoid with a bias 23, and in
-// groups 30 (floors 1.4 and 2.7).
+// 16384 x 256, k = 8, in a graph: bf16 scores 12 us, fp32 16, sigmoid with a bias 24,
+// and in groups 30 (floors 1.4 and 2.7).
 //
 // Equal results whatever the rounding: fp32 keys, their last 5 bits replaced by
 // the place in the lane, decide only when neighbours in the order lie further
-// apart than that and the fp32 error can reach, or are truly equal.  Where they
-// do not (about 1 token in 60 at 256 sigmoid scores) the candidates are put in
-// order by fp64 keys; where that does not settle it, all experts are.  Without a
+// apart than that and the fp32 error can reach, or are truly equal (at the cut the
+// error of any score there may be, since what is left out may have a large one and a
+// bias that takes it away).  Where they do not (about 1 token in 60 at 256 sigmoid
+// scores) the candidates are put in order by fp64 keys; where that does not settle
+// it, all experts are.  Without a
 // bias and without sums of two keys the order of the keys is the order of the
 // scores, which 16-bit scores show exactly.
 #include <cuda_bf16.h>
